@@ -247,7 +247,7 @@ def _plain_scan(s):
     dh = s["dh"] if s["dh"] is not None else x.new_zeros(N, C)
     prev = torch.cat([h[:1], h[:-1]])       # the state before each token
     prev[first] = h0[full]
-    lam = s["dy"].float()
+    lam = s["dy"].float().clone()           # .float() of 32 bits is the input itself
     lam[last] += dh[full]
     passed = torch.cat([a[1:], a[:1]])      # what token t+1 passes back to t
     passed[last] = 0.0
