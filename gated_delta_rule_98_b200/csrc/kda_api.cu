@@ -104,6 +104,103 @@ Offsets4 conv_offsets(size_t fw, size_t tok, int32_t dk, int32_t dv, size_t elt)
   return o;
 }
 
+bool opt_aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+// Checks of the packed [T, channels] entry points (gated scan).
+kda_status check_scan(const void* x, const void* gate, const int32_t* cu, int32_t N, int32_t T,
+                      int32_t max_len, int32_t channels, kda_dtype dt, const void* out,
+                      const void* ws, size_t ws_bytes) {
+  if (dt != KDA_F32 && dt != KDA_BF16) return KDA_ERR_UNSUPPORTED;
+  if (channels < 8 || channels % 8 != 0) return KDA_ERR_UNSUPPORTED;
+  if (N < 0 || T < 0 || max_len < 0) return KDA_ERR_INVALID_ARG;
+  if (!cu && (int64_t)N * max_len != T) return KDA_ERR_INVALID_ARG;
+  if (N == 0 && T > 0) return KDA_ERR_INVALID_ARG;
+  if (!opt_aligned4(cu)) return KDA_ERR_INVALID_ARG;
+  if (T > 0 && (!x || !gate || !out)) return KDA_ERR_INVALID_ARG;
+  if (!opt_aligned16(x) || !opt_aligned16(gate) || !opt_aligned16(out)) return KDA_ERR_INVALID_ARG;
+  const size_t need = kda_gated_scan_workspace_size(T, channels);
+  if (need == 0) return KDA_ERR_UNSUPPORTED;
+  if (!ws || !aligned16(ws) || ws_bytes < need) return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
+kda_status scan_common(const void* x, const void* z, const float* A, const float* g,
+                       const float* h0, const int32_t* cu, int32_t N, int32_t T, int32_t max_len,
+                       int32_t channels, kda_dtype dt, void* y, float* h_final, float* states,
+                       void* ws, size_t ws_bytes, kda_stream_t stream) {
+  kda_status st = check_scan(x, z ? z : (const void*)g, cu, N, T, max_len, channels, dt, y, ws,
+                             ws_bytes);
+  if (st != KDA_OK) return st;
+  if (!opt_aligned16(A) || !opt_aligned16(h0) || !opt_aligned16(h_final) ||
+      !opt_aligned16(states))
+    return KDA_ERR_INVALID_ARG;
+  if (N == 0) return KDA_OK;
+  kda::ScanArgs a{x, z, A, g, h0, cu, N, T, max_len, channels, dt == KDA_BF16,
+                  y, h_final, states, ws, (cudaStream_t)stream};
+  return kda::launch_scan(a) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status scan_backward_common(const void* x, const void* z, const float* A, const float* g,
+                                const float* states, const float* h0, const int32_t* cu,
+                                int32_t N, int32_t T, int32_t max_len, int32_t channels,
+                                kda_dtype dt, const void* dy, const float* dh_final, void* dx,
+                                void* dz, float* dg, float* dA, float* dh0, void* ws,
+                                size_t ws_bytes, kda_stream_t stream) {
+  kda_status st = check_scan(x, z ? z : (const void*)g, cu, N, T, max_len, channels, dt, dx, ws,
+                             ws_bytes);
+  if (st != KDA_OK) return st;
+  if (T > 0 && (!states || !dy || (z ? !dz : !dg))) return KDA_ERR_INVALID_ARG;
+  if (!opt_aligned16(A) || !opt_aligned16(h0) || !opt_aligned16(states) || !opt_aligned16(dy) ||
+      !opt_aligned16(dh_final) || !opt_aligned16(dz) || !opt_aligned16(dg) ||
+      !opt_aligned16(dA) || !opt_aligned16(dh0))
+    return KDA_ERR_INVALID_ARG;
+  if (N == 0) {
+    if (dA && cudaMemsetAsync(dA, 0, (size_t)channels * sizeof(float), (cudaStream_t)stream) !=
+                  cudaSuccess)
+      return KDA_ERR_CUDA;
+    return KDA_OK;
+  }
+  kda::ScanArgs a{x, z, A, g, h0, cu, N, T, max_len, channels, dt == KDA_BF16,
+                  nullptr, nullptr, const_cast<float*>(states), ws, (cudaStream_t)stream};
+  a.dy = dy;
+  a.dh_final = dh_final;
+  a.dx = dx;
+  a.dz = dz;
+  a.dg = dg;
+  a.dA = dA;
+  a.dh0 = dh0;
+  return kda::launch_scan_backward(a) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+// One side (queries or keys) of the norm-and-rotation entry points: pointers
+// and token strides of its [T, heads, d] tensors.
+bool qk_tensor_ok(bool work, const void* p, int64_t stride, int64_t row) {
+  if (!opt_aligned16(p)) return false;
+  return !work || (p && stride >= row && stride % 8 == 0);
+}
+
+kda_status check_qk(const kda::QkArgs& a, kda_dtype dt, bool backward) {
+  if (dt != KDA_F32 && dt != KDA_BF16) return KDA_ERR_UNSUPPORTED;
+  if (!dim_ok(a.d)) return KDA_ERR_UNSUPPORTED;
+  if (a.rot < 0 || a.rot > a.d || a.rot % 8 != 0) return KDA_ERR_UNSUPPORTED;
+  if (a.T < 0 || a.side[0].heads < 0 || a.side[1].heads < 0) return KDA_ERR_INVALID_ARG;
+  if (!(a.eps >= 0.f && a.eps <= 3.0e38f)) return KDA_ERR_INVALID_ARG;
+  bool work = false;
+  for (const kda::QkSide& s : a.side) {
+    const bool w = a.T > 0 && s.heads > 0;
+    const int64_t row = (int64_t)s.heads * a.d;
+    work = work || w;
+    if (row > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    if (!qk_tensor_ok(w, s.x, s.x_stride, row) || !qk_tensor_ok(w, s.out, s.out_stride, row) ||
+        (backward && !qk_tensor_ok(w, s.dout, s.dout_stride, row)) || !opt_aligned16(s.weight) ||
+        !opt_aligned4(s.dweight))
+      return KDA_ERR_INVALID_ARG;
+  }
+  if (work && (!a.positions || (a.rot > 0 && !a.freqs))) return KDA_ERR_INVALID_ARG;
+  if (!opt_aligned4(a.positions) || ((uintptr_t)a.freqs & 7u)) return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
 kda_status forward_common(kda::ForwardArgs& a) {
   // A clean error word for this call, stream-ordered before its first kernel:
   // the kernels only OR errors into it, so no report of one CTA can be wiped
@@ -347,6 +444,169 @@ kda_status kda_short_conv_swish(const void* x, const float* w, const int32_t* cu
   a.bf16 = dt == KDA_BF16;
   a.stream = (cudaStream_t)stream;
   return kda::launch_conv_swish(a) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_short_conv_swish_backward_workspace_size(int32_t total_tokens, int32_t channels,
+                                                    int32_t width) {
+  if (total_tokens < 0 || channels < 8 || channels % 8 != 0 || width < 1 || width > 4) return 0;
+  return kda::conv_backward_workspace_bytes(total_tokens, channels, width);
+}
+
+kda_status kda_short_conv_swish_backward(const void* x, const float* w, const void* dy,
+                                         const int32_t* cu_seqlens, int32_t num_seqs,
+                                         int32_t total_tokens, int32_t max_seqlen,
+                                         int32_t channels, int32_t width, kda_dtype dt, void* dx,
+                                         float* dw, void* workspace, size_t workspace_bytes,
+                                         kda_stream_t stream) {
+  const NvtxRange nvtx_range_("kda_short_conv_swish_backward");
+  if (dt != KDA_F32 && dt != KDA_BF16) return KDA_ERR_UNSUPPORTED;
+  if (width < 1 || width > 4) return KDA_ERR_UNSUPPORTED;
+  if (channels < 8 || channels % 8 != 0) return KDA_ERR_UNSUPPORTED;
+  if (num_seqs < 0 || total_tokens < 0 || max_seqlen < 0) return KDA_ERR_INVALID_ARG;
+  if (!cu_seqlens && (int64_t)num_seqs * max_seqlen != total_tokens) return KDA_ERR_INVALID_ARG;
+  if (total_tokens > 0 && num_seqs == 0) return KDA_ERR_INVALID_ARG;
+  if (!w || !dw || !opt_aligned4(w) || !opt_aligned4(dw) || !opt_aligned4(cu_seqlens))
+    return KDA_ERR_INVALID_ARG;
+  if (total_tokens > 0 && (!x || !dy || !dx)) return KDA_ERR_INVALID_ARG;
+  if (!opt_aligned16(x) || !opt_aligned16(dy) || !opt_aligned16(dx)) return KDA_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes <
+          kda_short_conv_swish_backward_workspace_size(total_tokens, channels, width))
+    return KDA_ERR_INVALID_ARG;
+  kda::ConvBackwardArgs a{x, dy, w, cu_seqlens, num_seqs, total_tokens, max_seqlen, channels,
+                          width, dt == KDA_BF16, dx, dw, workspace, (cudaStream_t)stream};
+  return kda::launch_conv_swish_backward(a) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_gated_scan_workspace_size(int32_t total_tokens, int32_t channels) {
+  if (total_tokens < 0 || channels < 8 || channels % 8 != 0) return 0;
+  return kda::scan_workspace_bytes(total_tokens, channels);
+}
+
+kda_status kda_gated_scan(const void* x, const void* z, const float* A, const float* h0,
+                          const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                          int32_t max_seqlen, int32_t channels, kda_dtype dt, void* y,
+                          float* h_final, float* states, void* workspace,
+                          size_t workspace_bytes, kda_stream_t stream) {
+  const NvtxRange nvtx_range_("kda_gated_scan");
+  if (total_tokens > 0 && (!z || !A)) return KDA_ERR_INVALID_ARG;
+  return scan_common(x, z, A, nullptr, h0, cu_seqlens, num_seqs, total_tokens, max_seqlen,
+                     channels, dt, y, h_final, states, workspace, workspace_bytes, stream);
+}
+
+kda_status kda_gated_scan_g(const void* x, const float* g, const float* h0,
+                            const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                            int32_t max_seqlen, int32_t channels, kda_dtype dt, void* y,
+                            float* h_final, float* states, void* workspace,
+                            size_t workspace_bytes, kda_stream_t stream) {
+  const NvtxRange nvtx_range_("kda_gated_scan_g");
+  if (total_tokens > 0 && !g) return KDA_ERR_INVALID_ARG;
+  return scan_common(x, nullptr, nullptr, g, h0, cu_seqlens, num_seqs, total_tokens, max_seqlen,
+                     channels, dt, y, h_final, states, workspace, workspace_bytes, stream);
+}
+
+kda_status kda_gated_scan_backward(const void* x, const void* z, const float* A,
+                                   const float* states, const float* h0,
+                                   const int32_t* cu_seqlens, int32_t num_seqs,
+                                   int32_t total_tokens, int32_t max_seqlen, int32_t channels,
+                                   kda_dtype dt, const void* dy, const float* dh_final, void* dx,
+                                   void* dz, float* dA, float* dh0, void* workspace,
+                                   size_t workspace_bytes, kda_stream_t stream) {
+  const NvtxRange nvtx_range_("kda_gated_scan_backward");
+  if (!dA || (total_tokens > 0 && (!z || !A))) return KDA_ERR_INVALID_ARG;
+  return scan_backward_common(x, z, A, nullptr, states, h0, cu_seqlens, num_seqs, total_tokens,
+                              max_seqlen, channels, dt, dy, dh_final, dx, dz, nullptr, dA, dh0,
+                              workspace, workspace_bytes, stream);
+}
+
+kda_status kda_gated_scan_g_backward(const void* x, const float* g, const float* states,
+                                     const float* h0, const int32_t* cu_seqlens,
+                                     int32_t num_seqs, int32_t total_tokens, int32_t max_seqlen,
+                                     int32_t channels, kda_dtype dt, const void* dy,
+                                     const float* dh_final, void* dx, float* dg, float* dh0,
+                                     void* workspace, size_t workspace_bytes,
+                                     kda_stream_t stream) {
+  const NvtxRange nvtx_range_("kda_gated_scan_g_backward");
+  if (total_tokens > 0 && !g) return KDA_ERR_INVALID_ARG;
+  return scan_backward_common(x, nullptr, nullptr, g, states, h0, cu_seqlens, num_seqs,
+                              total_tokens, max_seqlen, channels, dt, dy, dh_final, dx, nullptr,
+                              dg, nullptr, dh0, workspace, workspace_bytes, stream);
+}
+
+kda_status kda_gated_scan_step(const void* x, const void* z, const float* A, float* h_inout,
+                               int32_t B, int32_t channels, kda_dtype dt, void* y,
+                               kda_stream_t stream) {
+  const NvtxRange nvtx_range_("kda_gated_scan_step");
+  if (dt != KDA_F32 && dt != KDA_BF16) return KDA_ERR_UNSUPPORTED;
+  if (channels < 8 || channels % 8 != 0) return KDA_ERR_UNSUPPORTED;
+  if (B < 0) return KDA_ERR_INVALID_ARG;
+  if (B == 0) return KDA_OK;
+  if (!x || !z || !A || !h_inout || !y) return KDA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(z) || !aligned16(A) || !aligned16(h_inout) || !aligned16(y))
+    return KDA_ERR_INVALID_ARG;
+  return kda::launch_scan_step(x, z, A, h_inout, B, channels, dt == KDA_BF16, y,
+                               (cudaStream_t)stream) == cudaSuccess
+             ? KDA_OK
+             : KDA_ERR_CUDA;
+}
+
+kda_status kda_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const int32_t* positions, const double* freqs,
+                            const float* q_weight, const float* k_weight, float eps,
+                            int32_t total_tokens, int32_t Hq, int32_t Hk, int32_t d, int32_t rot,
+                            int32_t interleaved, kda_dtype dt, void* q_out, int64_t q_out_stride,
+                            void* k_out, int64_t k_out_stride, kda_stream_t stream) {
+  const NvtxRange nvtx_range_("kda_qk_norm_rope");
+  kda::QkArgs a{};
+  a.side[0] = {q, nullptr, q_out, q_weight, nullptr, q_stride, 0, q_out_stride, Hq};
+  a.side[1] = {k, nullptr, k_out, k_weight, nullptr, k_stride, 0, k_out_stride, Hk};
+  a.positions = positions;
+  a.freqs = freqs;
+  a.eps = eps;
+  a.T = total_tokens;
+  a.d = d;
+  a.rot = rot;
+  a.interleaved = interleaved != 0;
+  a.bf16 = dt == KDA_BF16;
+  a.stream = (cudaStream_t)stream;
+  kda_status st = check_qk(a, dt, false);
+  if (st != KDA_OK) return st;
+  if (total_tokens == 0 || (Hq == 0 && Hk == 0)) return KDA_OK;
+  return kda::launch_qk_norm_rope(a) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_qk_norm_rope_backward_workspace_size(int32_t total_tokens, int32_t d) {
+  if (total_tokens < 0 || !dim_ok(d)) return 0;
+  return kda::qk_backward_workspace_bytes(total_tokens, d);
+}
+
+kda_status kda_qk_norm_rope_backward(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* dq_out,
+    int64_t dq_out_stride, const void* dk_out, int64_t dk_out_stride, const int32_t* positions,
+    const double* freqs, const float* q_weight, const float* k_weight, float eps,
+    int32_t total_tokens, int32_t Hq, int32_t Hk, int32_t d, int32_t rot, int32_t interleaved,
+    kda_dtype dt, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride, float* dq_weight,
+    float* dk_weight, void* workspace, size_t workspace_bytes, kda_stream_t stream) {
+  const NvtxRange nvtx_range_("kda_qk_norm_rope_backward");
+  kda::QkArgs a{};
+  a.side[0] = {q, dq_out, dq, q_weight, dq_weight, q_stride, dq_out_stride, dq_stride, Hq};
+  a.side[1] = {k, dk_out, dk, k_weight, dk_weight, k_stride, dk_out_stride, dk_stride, Hk};
+  a.positions = positions;
+  a.freqs = freqs;
+  a.eps = eps;
+  a.T = total_tokens;
+  a.d = d;
+  a.rot = rot;
+  a.interleaved = interleaved != 0;
+  a.bf16 = dt == KDA_BF16;
+  a.ws = workspace;
+  a.stream = (cudaStream_t)stream;
+  kda_status st = check_qk(a, dt, true);
+  if (st != KDA_OK) return st;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < kda_qk_norm_rope_backward_workspace_size(total_tokens, d))
+    return KDA_ERR_INVALID_ARG;
+  return kda::launch_qk_norm_rope_backward(a) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 size_t kda_forward_conv_workspace_size(int32_t num_seqs, int32_t total_tokens,

@@ -11,6 +11,8 @@ with torch, check every tensor's shape and dtype against its role, and pass
 the current stream: ``forward``, ``forward_g``, ``forward_scalar_gate``,
 ``forward_checkpoints``, ``forward_norm_gate``, ``forward_conv``,
 ``short_conv_swish``, ``decode_step``, ``decode_step_norm_gate``,
+``short_conv_swish_backward``, ``gated_scan`` / ``gated_scan_g`` and their
+``_backward``, ``gated_scan_step``, ``qk_norm_rope`` and its ``_backward``,
 ``cp_local`` / ``cp_finish`` / ``state_compose`` (context parallelism; the
 collective lives in ``cp.py``), ``workspace`` and ``check_device_error``.
 """
@@ -35,7 +37,15 @@ EXPORTS = ("kda_status_string", "kda_version", "kda_forward_workspace_size",
            "kda_forward_norm_gate", "kda_decode_step_norm_gate", "kda_forward_scalar_gate",
            "kda_short_conv_swish", "kda_forward_conv_workspace_size", "kda_forward_conv",
            "kda_cp_workspace_size", "kda_cp_local", "kda_cp_finish", "kda_state_compose",
-           "kda_check_device_error", "kda_debug_set_wait_limit", "kda_decode_step_conv")
+           "kda_check_device_error", "kda_debug_set_wait_limit", "kda_decode_step_conv",
+           "kda_short_conv_swish_backward_workspace_size", "kda_short_conv_swish_backward",
+           "kda_gated_scan_workspace_size", "kda_gated_scan", "kda_gated_scan_g",
+           "kda_gated_scan_backward", "kda_gated_scan_g_backward", "kda_gated_scan_step",
+           "kda_qk_norm_rope", "kda_qk_norm_rope_backward_workspace_size",
+           "kda_qk_norm_rope_backward")
+
+# Tokens between the states that the gated scan saves for its gradient.
+KDA_SCAN_INTERVAL = 64
 
 # Bytes of the library's fixed scratch array used by kda_forward_noalloc.
 KDA_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -92,6 +102,35 @@ def lib():
     L.kda_decode_step_conv.restype = ctypes.c_int
     L.kda_short_conv_swish.argtypes = [vp, vp, vp] + [i32] * 5 + [ctypes.c_int, vp, vp]
     L.kda_short_conv_swish.restype = ctypes.c_int
+    L.kda_short_conv_swish_backward_workspace_size.argtypes = [i32] * 3
+    L.kda_short_conv_swish_backward_workspace_size.restype = sz
+    L.kda_short_conv_swish_backward.argtypes = ([vp] * 4 + [i32] * 5 +
+                                                [ctypes.c_int, vp, vp, vp, sz, vp])
+    L.kda_short_conv_swish_backward.restype = ctypes.c_int
+    L.kda_gated_scan_workspace_size.argtypes = [i32] * 2
+    L.kda_gated_scan_workspace_size.restype = sz
+    L.kda_gated_scan.argtypes = [vp] * 5 + [i32] * 4 + [ctypes.c_int] + [vp] * 4 + [sz, vp]
+    L.kda_gated_scan.restype = ctypes.c_int
+    L.kda_gated_scan_g.argtypes = [vp] * 4 + [i32] * 4 + [ctypes.c_int] + [vp] * 4 + [sz, vp]
+    L.kda_gated_scan_g.restype = ctypes.c_int
+    L.kda_gated_scan_backward.argtypes = ([vp] * 6 + [i32] * 4 + [ctypes.c_int] + [vp] * 7 +
+                                          [sz, vp])
+    L.kda_gated_scan_backward.restype = ctypes.c_int
+    L.kda_gated_scan_g_backward.argtypes = ([vp] * 5 + [i32] * 4 + [ctypes.c_int] + [vp] * 6 +
+                                            [sz, vp])
+    L.kda_gated_scan_g_backward.restype = ctypes.c_int
+    L.kda_gated_scan_step.argtypes = [vp] * 4 + [i32] * 2 + [ctypes.c_int, vp, vp]
+    L.kda_gated_scan_step.restype = ctypes.c_int
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    L.kda_qk_norm_rope.argtypes = ([vp, i64, vp, i64] + [vp] * 4 + [f32] + [i32] * 6 +
+                                   [ctypes.c_int, vp, i64, vp, i64, vp])
+    L.kda_qk_norm_rope.restype = ctypes.c_int
+    L.kda_qk_norm_rope_backward_workspace_size.argtypes = [i32] * 2
+    L.kda_qk_norm_rope_backward_workspace_size.restype = sz
+    L.kda_qk_norm_rope_backward.argtypes = ([vp, i64] * 4 + [vp] * 4 + [f32] + [i32] * 6 +
+                                            [ctypes.c_int, vp, i64, vp, i64] + [vp] * 3 +
+                                            [sz, vp])
+    L.kda_qk_norm_rope_backward.restype = ctypes.c_int
     L.kda_forward_conv_workspace_size.argtypes = [i32] * 6 + [ctypes.c_int, i32]
     L.kda_forward_conv_workspace_size.restype = sz
     L.kda_forward_conv.argtypes = ([vp] * 6 + [i32] + [vp] * 5 + [i32] * 6 +
@@ -197,6 +236,79 @@ def kda_short_conv_swish(x, w, cu_seqlens, num_seqs, total_tokens, max_seqlen, c
                          dt, y, stream):
     return lib().kda_short_conv_swish(x, w, cu_seqlens, num_seqs, total_tokens, max_seqlen,
                                       channels, width, dt, y, stream)
+
+
+def kda_short_conv_swish_backward_workspace_size(total_tokens, channels, width):
+    return lib().kda_short_conv_swish_backward_workspace_size(total_tokens, channels, width)
+
+
+def kda_short_conv_swish_backward(x, w, dy, cu_seqlens, num_seqs, total_tokens, max_seqlen,
+                                  channels, width, dt, dx, dw, workspace, workspace_bytes,
+                                  stream):
+    return lib().kda_short_conv_swish_backward(x, w, dy, cu_seqlens, num_seqs, total_tokens,
+                                               max_seqlen, channels, width, dt, dx, dw,
+                                               workspace, workspace_bytes, stream)
+
+
+def kda_gated_scan_workspace_size(total_tokens, channels):
+    return lib().kda_gated_scan_workspace_size(total_tokens, channels)
+
+
+def kda_gated_scan(x, z, A, h0, cu_seqlens, num_seqs, total_tokens, max_seqlen, channels, dt, y,
+                   h_final, states, workspace, workspace_bytes, stream):
+    return lib().kda_gated_scan(x, z, A, h0, cu_seqlens, num_seqs, total_tokens, max_seqlen,
+                                channels, dt, y, h_final, states, workspace, workspace_bytes,
+                                stream)
+
+
+def kda_gated_scan_g(x, g, h0, cu_seqlens, num_seqs, total_tokens, max_seqlen, channels, dt, y,
+                     h_final, states, workspace, workspace_bytes, stream):
+    return lib().kda_gated_scan_g(x, g, h0, cu_seqlens, num_seqs, total_tokens, max_seqlen,
+                                  channels, dt, y, h_final, states, workspace, workspace_bytes,
+                                  stream)
+
+
+def kda_gated_scan_backward(x, z, A, states, h0, cu_seqlens, num_seqs, total_tokens, max_seqlen,
+                            channels, dt, dy, dh_final, dx, dz, dA, dh0, workspace,
+                            workspace_bytes, stream):
+    return lib().kda_gated_scan_backward(x, z, A, states, h0, cu_seqlens, num_seqs,
+                                         total_tokens, max_seqlen, channels, dt, dy, dh_final,
+                                         dx, dz, dA, dh0, workspace, workspace_bytes, stream)
+
+
+def kda_gated_scan_g_backward(x, g, states, h0, cu_seqlens, num_seqs, total_tokens, max_seqlen,
+                              channels, dt, dy, dh_final, dx, dg, dh0, workspace,
+                              workspace_bytes, stream):
+    return lib().kda_gated_scan_g_backward(x, g, states, h0, cu_seqlens, num_seqs, total_tokens,
+                                           max_seqlen, channels, dt, dy, dh_final, dx, dg, dh0,
+                                           workspace, workspace_bytes, stream)
+
+
+def kda_gated_scan_step(x, z, A, h_inout, B, channels, dt, y, stream):
+    return lib().kda_gated_scan_step(x, z, A, h_inout, B, channels, dt, y, stream)
+
+
+def kda_qk_norm_rope(q, q_stride, k, k_stride, positions, freqs, q_weight, k_weight, eps,
+                     total_tokens, Hq, Hk, d, rot, interleaved, dt, q_out, q_out_stride, k_out,
+                     k_out_stride, stream):
+    return lib().kda_qk_norm_rope(q, q_stride, k, k_stride, positions, freqs, q_weight, k_weight,
+                                  eps, total_tokens, Hq, Hk, d, rot, interleaved, dt, q_out,
+                                  q_out_stride, k_out, k_out_stride, stream)
+
+
+def kda_qk_norm_rope_backward_workspace_size(total_tokens, d):
+    return lib().kda_qk_norm_rope_backward_workspace_size(total_tokens, d)
+
+
+def kda_qk_norm_rope_backward(q, q_stride, k, k_stride, dq_out, dq_out_stride, dk_out,
+                              dk_out_stride, positions, freqs, q_weight, k_weight, eps,
+                              total_tokens, Hq, Hk, d, rot, interleaved, dt, dq, dq_stride, dk,
+                              dk_stride, dq_weight, dk_weight, workspace, workspace_bytes,
+                              stream):
+    return lib().kda_qk_norm_rope_backward(
+        q, q_stride, k, k_stride, dq_out, dq_out_stride, dk_out, dk_out_stride, positions, freqs,
+        q_weight, k_weight, eps, total_tokens, Hq, Hk, d, rot, interleaved, dt, dq, dq_stride,
+        dk, dk_stride, dq_weight, dk_weight, workspace, workspace_bytes, stream)
 
 
 def kda_forward_conv_workspace_size(num_seqs, total_tokens, max_seqlen, H, dk, dv, dt, chunk):
@@ -532,6 +644,251 @@ def short_conv_swish(x, w, *, cu_seqlens=None, num_seqs=None, max_seqlen=None, y
     if st != KDA_OK:
         raise KdaError(st, "kda_short_conv_swish")
     return y
+
+
+def _packed(x, cu_seqlens, num_seqs, max_seqlen):
+    """(tokens, channels, sequences, longest) of a packed [T, ...] tensor."""
+    T = x.shape[0]
+    C = x.numel() // T if T else int(np.prod(x.shape[1:]))
+    if cu_seqlens is None:
+        N = 1 if num_seqs is None else int(num_seqs)
+        return T, C, N, T // N if N else 0
+    if max_seqlen is None:
+        raise ValueError("max_seqlen is required with cu_seqlens")
+    return T, C, cu_seqlens.numel() - 1, int(max_seqlen)
+
+
+def _roles(device, **ts):
+    """Raise ValueError unless every tensor given is on ``device``, contiguous and
+    of its role's (shape, dtype); ts: name = (tensor, shape, dtype)."""
+    for name, (t, shape, dtype) in ts.items():
+        if t is None:
+            continue
+        if t.device != device:
+            raise ValueError(f"{name}: on {t.device}, expected {device}")
+        if t.dtype != dtype or t.shape != shape:
+            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} "
+                             f"{dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+
+
+def _call(fn, device, stream, *args):
+    """Run a C entry point on the tensors' device and raise unless it returns KDA_OK."""
+    if device.type != "cuda":
+        raise ValueError("KDA runs on the GPU only: pass CUDA tensors")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(stream))
+    else:
+        st = fn(*args, _stream(stream))
+    if st != KDA_OK:
+        raise KdaError(st, fn.__name__)
+
+
+def _workspace_of(nbytes, ws, device, what):
+    if nbytes == 0:
+        raise KdaError(KDA_ERR_UNSUPPORTED, what)
+    if ws is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace: contiguous uint8 on {device} expected")
+    return ws
+
+
+def short_conv_swish_backward(x, w, dy, *, cu_seqlens=None, num_seqs=None, max_seqlen=None,
+                              dx=None, dw=None, workspace=None, stream=None):
+    """Gradient of short_conv_swish: dy is the gradient of y (x's shape and
+    dtype).  Returns (dx, dw), dw [channels, width] fp32.  Rows from
+    cu_seqlens[N] on (a padded batch) are left as they were in dx."""
+    T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
+    width = w.shape[-1]
+    dev, f32 = x.device, torch.float32
+    if dx is None:
+        dx = torch.empty_like(x)
+    if dw is None:
+        dw = torch.empty((C, width), dtype=f32, device=dev)
+    _roles(dev, x=(x, x.shape, x.dtype), w=(w, (C, width), f32), dy=(dy, x.shape, x.dtype),
+           dx=(dx, x.shape, x.dtype), dw=(dw, (C, width), f32),
+           cu_seqlens=(cu_seqlens, (N + 1,), torch.int32))
+    ws = _workspace_of(kda_short_conv_swish_backward_workspace_size(T, C, width), workspace, dev,
+                       "kda_short_conv_swish_backward_workspace_size")
+    _call(kda_short_conv_swish_backward, dev, stream, _p(x), _p(w), _p(dy), _p(cu_seqlens), N, T,
+          L, C, width, _dt(x), _p(dx), _p(dw), _p(ws), ws.numel())
+    return dx, dw
+
+
+def _gated_scan(x, z, A, g, h0, cu_seqlens, num_seqs, max_seqlen, y, h_final, states,
+                save_states, ws, stream):
+    T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
+    dev, f32 = x.device, torch.float32
+    if y is None:
+        y = torch.empty_like(x)
+    if h_final is None:
+        h_final = torch.empty((N, C), dtype=f32, device=dev)
+    rows = (T + KDA_SCAN_INTERVAL - 1) // KDA_SCAN_INTERVAL
+    if states is None and save_states:
+        states = torch.empty((rows, C), dtype=f32, device=dev)
+    _roles(dev, x=(x, x.shape, x.dtype), z=(z, x.shape, x.dtype), A=(A, (C,), f32),
+           g=(g, x.shape, f32), h0=(h0, (N, C), f32), y=(y, x.shape, x.dtype),
+           h_final=(h_final, (N, C), f32), states=(states, (rows, C), f32),
+           cu_seqlens=(cu_seqlens, (N + 1,), torch.int32))
+    ws = _workspace_of(kda_gated_scan_workspace_size(T, C), ws, dev,
+                       "kda_gated_scan_workspace_size")
+    gate = (_p(g),) if z is None else (_p(z), _p(A))
+    _call(kda_gated_scan_g if z is None else kda_gated_scan, dev, stream, _p(x), *gate, _p(h0),
+          _p(cu_seqlens), N, T, L, C, _dt(x), _p(y), _p(h_final), _p(states), _p(ws),
+          ws.numel())
+    return (y, h_final) if states is None else (y, h_final, states)
+
+
+def gated_scan(x, z, A, *, h0=None, cu_seqlens=None, num_seqs=None, max_seqlen=None,
+               save_states=False, y=None, h_final=None, states=None, workspace=None,
+               stream=None):
+    """Gated linear recurrence over packed sequences, one number of state per
+    channel: a = exp(-5 sigmoid(e^A z)), h_t = a h_{t-1} + (1 - a) x_t.  x, z
+    [T, ...] (trailing axes = channels) in one dtype, A [channels] fp32, h0
+    [N, channels] fp32 or None.  Returns (y, h_final), and with ``save_states``
+    also the states that gated_scan_backward needs,
+    [ceil(T / KDA_SCAN_INTERVAL), channels] fp32.  Rows from cu_seqlens[N] on
+    (a padded batch) are left as they were in y."""
+    return _gated_scan(x, z, A, None, h0, cu_seqlens, num_seqs, max_seqlen, y, h_final, states,
+                       save_states, workspace, stream)
+
+
+def gated_scan_g(x, g, *, h0=None, cu_seqlens=None, num_seqs=None, max_seqlen=None,
+                 save_states=False, y=None, h_final=None, states=None, workspace=None,
+                 stream=None):
+    """gated_scan with the fp32 log-decay g (x's shape) given directly and the
+    input unscaled: h_t = exp(g_t) h_{t-1} + x_t."""
+    return _gated_scan(x, None, None, g, h0, cu_seqlens, num_seqs, max_seqlen, y, h_final,
+                       states, save_states, workspace, stream)
+
+
+def _gated_scan_backward(x, z, A, g, states, dy, h0, dh_final, cu_seqlens, num_seqs, max_seqlen,
+                         ws, stream):
+    T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
+    dev, f32 = x.device, torch.float32
+    rows = (T + KDA_SCAN_INTERVAL - 1) // KDA_SCAN_INTERVAL
+    _roles(dev, x=(x, x.shape, x.dtype), z=(z, x.shape, x.dtype), A=(A, (C,), f32),
+           g=(g, x.shape, f32), states=(states, (rows, C), f32), dy=(dy, x.shape, x.dtype),
+           h0=(h0, (N, C), f32), dh_final=(dh_final, (N, C), f32),
+           cu_seqlens=(cu_seqlens, (N + 1,), torch.int32))
+    dx, dh0 = torch.empty_like(x), torch.empty((N, C), dtype=f32, device=dev)
+    ws = _workspace_of(kda_gated_scan_workspace_size(T, C), ws, dev,
+                       "kda_gated_scan_workspace_size")
+    if z is None:
+        dg = torch.empty_like(g)
+        _call(kda_gated_scan_g_backward, dev, stream, _p(x), _p(g), _p(states), _p(h0),
+              _p(cu_seqlens), N, T, L, C, _dt(x), _p(dy), _p(dh_final), _p(dx), _p(dg), _p(dh0),
+              _p(ws), ws.numel())
+        return dx, dg, dh0
+    dz, dA = torch.empty_like(z), torch.empty_like(A)
+    _call(kda_gated_scan_backward, dev, stream, _p(x), _p(z), _p(A), _p(states), _p(h0),
+          _p(cu_seqlens), N, T, L, C, _dt(x), _p(dy), _p(dh_final), _p(dx), _p(dz), _p(dA),
+          _p(dh0), _p(ws), ws.numel())
+    return dx, dz, dA, dh0
+
+
+def gated_scan_backward(x, z, A, states, dy, *, h0=None, dh_final=None, cu_seqlens=None,
+                        num_seqs=None, max_seqlen=None, workspace=None, stream=None):
+    """Gradients of gated_scan: x, z, A, h0 and the packing as given to it,
+    states as it returned them, dy the gradient of y, dh_final [N, channels]
+    fp32 that of h_final (None: zeros).  Returns (dx, dz, dA, dh0)."""
+    return _gated_scan_backward(x, z, A, None, states, dy, h0, dh_final, cu_seqlens, num_seqs,
+                                max_seqlen, workspace, stream)
+
+
+def gated_scan_g_backward(x, g, states, dy, *, h0=None, dh_final=None, cu_seqlens=None,
+                          num_seqs=None, max_seqlen=None, workspace=None, stream=None):
+    """Gradients of gated_scan_g (see gated_scan_backward): (dx, dg, dh0)."""
+    return _gated_scan_backward(x, None, None, g, states, dy, h0, dh_final, cu_seqlens,
+                                num_seqs, max_seqlen, workspace, stream)
+
+
+def gated_scan_step(x, z, A, h, *, y=None, stream=None):
+    """One step of gated_scan for B sequences: x, z [B, ...], A [channels] fp32;
+    h [B, channels] fp32 is updated in place.  Returns y (x's shape and dtype)."""
+    B, C, _, _ = _packed(x, None, 1, None)
+    if y is None:
+        y = torch.empty_like(x)
+    f32 = torch.float32
+    _roles(x.device, x=(x, x.shape, x.dtype), z=(z, x.shape, x.dtype), A=(A, (C,), f32),
+           h=(h, (B, C), f32), y=(y, x.shape, x.dtype))
+    _call(kda_gated_scan_step, x.device, stream, _p(x), _p(z), _p(A), _p(h), B, C, _dt(x), _p(y))
+    return y
+
+
+def _head_rows(name, t, like, dtype, device):
+    """Token stride of a [T, heads, d] tensor whose heads lie side by side."""
+    if t.device != device or t.dtype != dtype or t.shape != like.shape or t.dim() != 3:
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected "
+                         f"{tuple(like.shape)} {dtype} on {device}")
+    T, H, d = t.shape
+    if t.numel() and ((d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: heads must lie side by side (strides {t.stride()})")
+    return t.stride(0) if T > 1 else H * d
+
+
+def _qk(q, k, positions, freqs, q_weight, k_weight):
+    dev, f32 = q.device, torch.float32
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}: [T, Hq, d] and [T, Hk, d] "
+                         "expected")
+    T, _, d = q.shape
+    _roles(dev, positions=(positions, (T,), torch.int32),
+           freqs=(freqs, (freqs.numel(),), torch.float64), q_weight=(q_weight, (d,), f32),
+           k_weight=(k_weight, (d,), f32))
+    return T, d, 2 * freqs.numel()
+
+
+def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e-6,
+                 interleaved=False, q_out=None, k_out=None, stream=None):
+    """RMS norm over d of every query head (q [T,Hq,d]) and key head (k
+    [T,Hk,d]) with gains q_weight, k_weight [d] fp32 (None: ones), then the
+    rotation by positions [T] int32 times freqs [rot/2] fp64 of the first rot
+    channels, paired (i, i + rot/2), or (2i, 2i+1) when ``interleaved``.  q and
+    k may be slices of one projection's output (heads side by side, any token
+    stride); q_out = q, k_out = k works in place.  Returns (q_out, k_out)."""
+    T, d, rot = _qk(q, k, positions, freqs, q_weight, k_weight)
+    dev, dt = q.device, q.dtype
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=dt, device=dev)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=dt, device=dev)
+    qs, ks = _head_rows("q", q, q, dt, dev), _head_rows("k", k, k, dt, dev)
+    qos, kos = _head_rows("q_out", q_out, q, dt, dev), _head_rows("k_out", k_out, k, dt, dev)
+    _call(kda_qk_norm_rope, dev, stream, _p(q), qs, _p(k), ks, _p(positions), _p(freqs),
+          _p(q_weight), _p(k_weight), float(eps), T, q.shape[1], k.shape[1], d, rot,
+          int(interleaved), _dt(q), _p(q_out), qos, _p(k_out), kos)
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q, k, dq_out, dk_out, positions, freqs, *, q_weight=None,
+                          k_weight=None, eps=1e-6, interleaved=False, dq=None, dk=None,
+                          workspace=None, stream=None):
+    """Gradients of qk_norm_rope: dq_out, dk_out are those of its outputs, the
+    rest as given to it; dq = dq_out, dk = dk_out works in place.  Returns
+    (dq, dk, dq_weight, dk_weight), the last two [d] fp32 or None where the
+    gain is None."""
+    T, d, rot = _qk(q, k, positions, freqs, q_weight, k_weight)
+    dev, dt = q.device, q.dtype
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=dt, device=dev)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=dt, device=dev)
+    s = [_head_rows(name, t, like, dt, dev) for name, t, like in
+         (("q", q, q), ("k", k, k), ("dq_out", dq_out, q), ("dk_out", dk_out, k), ("dq", dq, q),
+          ("dk", dk, k))]
+    dqw = None if q_weight is None else torch.empty_like(q_weight)
+    dkw = None if k_weight is None else torch.empty_like(k_weight)
+    ws = _workspace_of(kda_qk_norm_rope_backward_workspace_size(T, d), workspace, dev,
+                       "kda_qk_norm_rope_backward_workspace_size")
+    _call(kda_qk_norm_rope_backward, dev, stream, _p(q), s[0], _p(k), s[1], _p(dq_out), s[2],
+          _p(dk_out), s[3], _p(positions), _p(freqs), _p(q_weight), _p(k_weight), float(eps), T,
+          q.shape[1], k.shape[1], d, rot, int(interleaved), _dt(q), _p(dq), s[4], _p(dk), s[5],
+          _p(dqw), _p(dkw), _p(ws), ws.numel())
+    return dq, dk, dqw, dkw
 
 
 def forward_conv(x_q, x_k, x_v, w_q, w_k, w_v, z, A, beta, *, S0=None, cu_seqlens=None,

@@ -365,6 +365,190 @@ kda_status kda_short_conv_swish(const void* x, const float* w, const int32_t* cu
                                 int32_t channels, int32_t width, kda_dtype dt, void* y,
                                 kda_stream_t stream);
 
+/*
+ * Gradient of kda_short_conv_swish: with u and y as above, p = sigmoid(u) and
+ * dy the gradient of a loss with respect to y,
+ *
+ *   du[t,c] = dy[t,c] * p * (1 + u * (1 - p))
+ *   dx[s,c] = sum_j w[c, width-1-j] * du[s+j, c]      (s+j in s's sequence)
+ *   dw[c, width-1-j] = sum_t du[t,c] * x[t-j, c]      (t-j in t's sequence)
+ *
+ *  x, dy, dx : [T, channels] in `dt`; dx must not overlap x or dy.
+ *  w, dw     : [channels, width] float32 (4-byte aligned); dw is overwritten.
+ *  cu_seqlens, sizes : as in kda_short_conv_swish.  cu_seqlens[N] may lie
+ *              below total_tokens (a padded batch): rows from there on are
+ *              not read, take no part in dw, and dx keeps what it held there.
+ *  workspace : kda_short_conv_swish_backward_workspace_size bytes, 16-byte
+ *              aligned, as in kda_forward.
+ * u is recomputed from x.  Sums are float32 in a fixed order (bit-identical
+ * from call to call).  Two launches.
+ */
+size_t kda_short_conv_swish_backward_workspace_size(int32_t total_tokens, int32_t channels,
+                                                    int32_t width);
+kda_status kda_short_conv_swish_backward(const void* x, const float* w, const void* dy,
+                                         const int32_t* cu_seqlens, int32_t num_seqs,
+                                         int32_t total_tokens, int32_t max_seqlen,
+                                         int32_t channels, int32_t width, kda_dtype dt, void* dx,
+                                         float* dw, void* workspace, size_t workspace_bytes,
+                                         kda_stream_t stream);
+
+/*
+ * Gated linear recurrence: the operator's channel-wise gate on a state of one
+ * number per channel instead of a dk x dv matrix (the diagonal special case of
+ * a linear recurrence; no delta correction).  Per channel c of each sequence,
+ *
+ *   g_t = -5 * sigmoid(exp(A_c) * z_t),  a_t = exp(g_t)
+ *   h_t = a_t h_{t-1} + (1 - a_t) x_t,   y_t = h_t rounded to `dt`
+ *
+ * so h stays between the extremes of h0 and x.  1 - a_t is taken as
+ * -expm1(g_t).
+ *
+ *  x, z, y  : [T, channels] in `dt`; y must not overlap any input.
+ *  A        : [channels] float32, per-channel gate scale (exp(A) is used).
+ *  h0       : [N, channels] float32 or NULL (zeros).
+ *  h_final  : [N, channels] float32 or NULL (not wanted); may equal h0.  An
+ *             empty sequence passes h0 through.
+ *  states   : [ceil(T / KDA_SCAN_INTERVAL), channels] float32 or NULL: row j
+ *             receives the state entering packed token KDA_SCAN_INTERVAL * j
+ *             (unspecified where that token starts a sequence).  The backward
+ *             calls need it; it adds 4 bytes per channel to every 64 tokens.
+ *  cu_seqlens, num_seqs, total_tokens, max_seqlen : as in kda_forward, except
+ *             that cu_seqlens is not validated (a malformed one gives
+ *             undefined values, never an out-of-range access) and
+ *             cu_seqlens[N] may lie below total_tokens (a padded batch): rows
+ *             from there on are not read, and y keeps what it held there.
+ *  channels : a positive multiple of 8 (else KDA_ERR_UNSUPPORTED).
+ *  workspace: kda_gated_scan_workspace_size bytes, 16-byte aligned, as in
+ *             kda_forward.
+ * The state, the products of a and every sum are float32 in a fixed order
+ * (bit-identical from call to call).
+ */
+#define KDA_SCAN_INTERVAL 64
+size_t kda_gated_scan_workspace_size(int32_t total_tokens, int32_t channels);
+kda_status kda_gated_scan(const void* x, const void* z, const float* A, const float* h0,
+                          const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                          int32_t max_seqlen, int32_t channels, kda_dtype dt, void* y,
+                          float* h_final, float* states, void* workspace,
+                          size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * The recurrence with the log-decay given directly and the input unscaled:
+ *   h_t = exp(g_t) h_{t-1} + x_t
+ *  g : [T, channels] float32; meant for g <= 0 (-inf clears the state).
+ * Everything else is kda_gated_scan's.
+ */
+kda_status kda_gated_scan_g(const void* x, const float* g, const float* h0,
+                            const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                            int32_t max_seqlen, int32_t channels, kda_dtype dt, void* y,
+                            float* h_final, float* states, void* workspace,
+                            size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * Gradients of kda_gated_scan.  With dy and dh_final the gradients of a loss
+ * with respect to y and h_final, s = sigmoid(exp(A) z) and, backwards through
+ * each sequence,
+ *
+ *   l_t  = dy_t + a_{t+1} l_{t+1}          (the last token: dy_t + dh_final)
+ *   dx_t = (1 - a_t) l_t
+ *   dz_t = -5 s_t (1 - s_t) exp(A) a_t (h_{t-1} - x_t) l_t
+ *   dA   = sum over all tokens of dz_t z_t (before dz is rounded)
+ *   dh0  = a_first l_first                 (an empty sequence: dh_final)
+ *
+ *  x, z, A, h0, states, cu_seqlens, sizes : as given to (states: as written
+ *             by) the forward call; h_{t-1} is recomputed from the states.
+ *  dy       : [T, channels] in `dt`;  dh_final : [N, channels] float32 or NULL (zeros).
+ *  dx, dz   : [T, channels] in `dt`;  dA : [channels] float32, overwritten;
+ *  dh0      : [N, channels] float32 or NULL (not wanted); may equal dh_final.
+ *             Outputs must not overlap the other inputs.  Rows from
+ *             cu_seqlens[N] on keep what they held.
+ *  workspace: kda_gated_scan_workspace_size bytes.
+ */
+kda_status kda_gated_scan_backward(const void* x, const void* z, const float* A,
+                                   const float* states, const float* h0,
+                                   const int32_t* cu_seqlens, int32_t num_seqs,
+                                   int32_t total_tokens, int32_t max_seqlen, int32_t channels,
+                                   kda_dtype dt, const void* dy, const float* dh_final, void* dx,
+                                   void* dz, float* dA, float* dh0, void* workspace,
+                                   size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * Gradients of kda_gated_scan_g: dx_t = l_t, dg_t = a_t h_{t-1} l_t
+ * (dg : [T, channels] float32), dh0 as above.
+ */
+kda_status kda_gated_scan_g_backward(const void* x, const float* g, const float* states,
+                                     const float* h0, const int32_t* cu_seqlens,
+                                     int32_t num_seqs, int32_t total_tokens, int32_t max_seqlen,
+                                     int32_t channels, kda_dtype dt, const void* dy,
+                                     const float* dh_final, void* dx, float* dg, float* dh0,
+                                     void* workspace, size_t workspace_bytes,
+                                     kda_stream_t stream);
+
+/*
+ * One step of kda_gated_scan for B sequences: x, z, y [B, channels] in `dt`
+ * (y may equal x or z), h_inout [B, channels] float32 updated in place.  One
+ * launch; no workspace.
+ */
+kda_status kda_gated_scan_step(const void* x, const void* z, const float* A, float* h_inout,
+                               int32_t B, int32_t channels, kda_dtype dt, void* y,
+                               kda_stream_t stream);
+
+/*
+ * Norm of every query and key head with the position rotation in one pass.
+ * For each head row v of d numbers of token t,
+ *
+ *   n = v / sqrt(mean v^2 + eps) * weight
+ *   (n_a, n_b) <- (n_a cos w - n_b sin w, n_b cos w + n_a sin w),
+ *   w = positions[t] * freqs[i]   for the pairs i < rot / 2
+ *
+ * with (a, b) = (i, i + rot/2), or (2i, 2i+1) when `interleaved` is not 0; the
+ * channels from rot on are not turned.  The angle is formed and reduced in 64
+ * bits, so positions far from 0 keep their accuracy.
+ *
+ *  q, q_out : [T, Hq, d], k, k_out : [T, Hk, d] in `dt`; heads lie d elements
+ *             apart and tokens *_stride elements apart (at least heads * d, a
+ *             multiple of 8), so that they may be slices of one projection's
+ *             output.  16-byte aligned.  q_out may be q and k_out may be k
+ *             (same stride); any other overlap is undefined.
+ *  positions: [T] int32 (4-byte aligned).
+ *  freqs    : [rot/2] float64, radians per position (8-byte aligned; may be
+ *             NULL when rot is 0).
+ *  q_weight, k_weight : [d] float32 gains, 16-byte aligned, or NULL (ones).
+ *  eps      : finite, not negative.
+ *  T >= 0; Hq, Hk >= 0 (a side with no heads may be NULL); d in {32, 64, 128};
+ *  rot a multiple of 8, 0 <= rot <= d (else KDA_ERR_UNSUPPORTED).
+ * One launch; no workspace.  Decode is T = B tokens.
+ */
+kda_status kda_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const int32_t* positions, const double* freqs,
+                            const float* q_weight, const float* k_weight, float eps,
+                            int32_t total_tokens, int32_t Hq, int32_t Hk, int32_t d, int32_t rot,
+                            int32_t interleaved, kda_dtype dt, void* q_out, int64_t q_out_stride,
+                            void* k_out, int64_t k_out_stride, kda_stream_t stream);
+
+/*
+ * Gradients of kda_qk_norm_rope: with R the rotation, r = 1/sqrt(mean v^2 + eps),
+ * b = R^T dout and c = b * weight,
+ *
+ *   dv = r (c - v r^2 mean(c v)),   dweight = sum over tokens and heads of b v r
+ *
+ *  q, k, positions, freqs, weights, eps, sizes : as given to the forward call.
+ *  dq_out, dk_out : gradients of q_out, k_out, with their token strides.
+ *  dq, dk   : gradients of q, k, with their token strides; dq may be dq_out and
+ *             dk may be dk_out (same stride); any other overlap is undefined.
+ *  dq_weight, dk_weight : [d] float32, overwritten, or NULL (not wanted).
+ *  workspace: kda_qk_norm_rope_backward_workspace_size bytes, 16-byte aligned,
+ *             as in kda_forward.
+ * Sums are float32 in a fixed order.  One launch, two with weight gradients.
+ */
+size_t kda_qk_norm_rope_backward_workspace_size(int32_t total_tokens, int32_t d);
+kda_status kda_qk_norm_rope_backward(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* dq_out,
+    int64_t dq_out_stride, const void* dk_out, int64_t dk_out_stride, const int32_t* positions,
+    const double* freqs, const float* q_weight, const float* k_weight, float eps,
+    int32_t total_tokens, int32_t Hq, int32_t Hk, int32_t d, int32_t rot, int32_t interleaved,
+    kda_dtype dt, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride, float* dq_weight,
+    float* dk_weight, void* workspace, size_t workspace_bytes, kda_stream_t stream);
+
 /* Workspace bytes for kda_forward_conv: kda_forward's on the tensor-core
  * path (bf16, dk = dv = 128, chunk 64), where the prologue runs inside the
  * chunk preparation; elsewhere kda_forward's plus room for the prologue's q,

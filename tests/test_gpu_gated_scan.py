@@ -1,0 +1,249 @@
+"""Gated linear recurrence on the GPU (kda_gated_scan, kda_gated_scan_g, their
+gradients, kda_gated_scan_step) against the float64 oracle, within the bound
+that the oracle carries for a float32 evaluation."""
+import numpy as np
+import pytest
+import torch
+
+from gated_delta_rule_98_b200 import kda
+from layer_testutil import close, cu_of, cuda, draw
+from oracle import scan
+
+pytestmark = pytest.mark.gpu
+
+
+def make(lens, C, dtype, entry, seed=0, state=True, mean=-3.0, pad=0):
+    T, N = sum(lens), len(lens)
+    p = dict(x=draw(seed, dtype, T + pad, C), dy=draw(seed + 1, dtype, T + pad, C),
+             cu=cu_of(lens), L=max(lens), T=T)
+    if entry == "z":
+        p.update(z=draw(seed + 2, dtype, T + pad, C, mean=mean, std=1.5),
+                 A=draw(seed + 3, "f32", C, std=0.3))
+    else:
+        p["g"] = -torch.exp(draw(seed + 2, "f32", T + pad, C, mean=mean, std=1.5))
+    if state:
+        p.update(h0=draw(seed + 4, "f32", N, C), dh=draw(seed + 5, "f32", N, C))
+    return p
+
+
+def gate_of(p):
+    return (cuda(p["z"]), cuda(p["A"])) if "z" in p else (cuda(p["g"]),)
+
+
+def run(p, equal=None, **kw):
+    """(y, h_final, states), gradients; ``equal``: so many equal sequences without cu_seqlens."""
+    fwd, bwd = ((kda.gated_scan, kda.gated_scan_backward) if "z" in p else
+                (kda.gated_scan_g, kda.gated_scan_g_backward))
+    how = dict(num_seqs=equal) if equal else dict(cu_seqlens=cuda(p["cu"]), max_seqlen=p["L"])
+    x, gate, h0 = cuda(p["x"]), gate_of(p), cuda(p.get("h0"))
+    out = fwd(x, *gate, h0=h0, save_states=True, **how, **kw)
+    grads = bwd(x, *gate, out[2], cuda(p["dy"]), h0=h0, dh_final=cuda(p.get("dh")), **how)
+    torch.cuda.synchronize()
+    return out, grads
+
+
+def check(p, out, grads):
+    T = p["T"]
+    cu = p["cu"].tolist()
+    by = {k: p[k][:T] if k in "zg" else p[k] for k in ("z", "A", "g") if k in p}
+    f = scan.forward(p["x"][:T], cu, h0=p.get("h0"), **by)
+    b = scan.backward(p["x"][:T], cu, p["dy"][:T], h0=p.get("h0"), dh_final=p.get("dh"), **by)
+    close(out[0][:T], f["y"], f["e_y"], "y")
+    close(out[1], f["h_final"], f["e_h_final"], "h_final")
+    names = ("dx", "dz", "dA", "dh0") if "z" in p else ("dx", "dg", "dh0")
+    for name, got in zip(names, grads):
+        got = got[:T] if name in ("dx", "dz", "dg") else got
+        close(got, b[name], b["e_" + name], name)
+
+
+LENS = [
+    [1], [2], [63], [64], [65], [129], [1000],
+    [1, 1, 1, 1, 1], [0, 5, 0, 0, 64, 1, 0], [64, 64, 128], [63, 65, 1, 127, 200, 0],
+    [300, 31, 33, 500], [3] * 200,
+]
+
+
+@pytest.mark.parametrize("entry", ["z", "g"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", LENS, ids=lambda v: "_".join(map(str, v))[:24])
+def test_packed_lengths(lens, dtype, entry):
+    p = make(lens, 40, dtype, entry, seed=len(lens))
+    check(p, *run(p))
+
+
+@pytest.mark.parametrize("entry", ["z", "g"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [8, 16, 24, 72, 264, 2056])
+def test_channels(C, dtype, entry):
+    p = make([70, 0, 133], C, dtype, entry, seed=C, state=C % 3 == 0)
+    check(p, *run(p))
+
+
+@pytest.mark.parametrize("entry", ["z", "g"])
+@pytest.mark.parametrize("N,L", [(1, 5000), (3, 1700), (7, 1), (1, 9001)])
+def test_equal_sequences_and_long_axes(N, L, entry):
+    """Few channels over many tokens (the token axis is split over blocks), with long memories."""
+    p = make([L] * N, 16, "f32", entry, seed=N + L, mean=-5.0)
+    check(p, *run(p, equal=N))
+
+
+def test_long_packed_split():
+    p = make([2500, 0, 40, 3100, 1, 1, 1800], 24, "bf16", "z", seed=77, mean=-6.0)
+    check(p, *run(p))
+
+
+@pytest.mark.parametrize("entry", ["z", "g"])
+def test_padded_batch_leaves_rows_behind_the_last_sequence(entry):
+    p = make([70, 9], 24, "bf16", entry, seed=5, pad=60)
+    how = dict(cu_seqlens=cuda(p["cu"]), max_seqlen=p["L"])
+    x, gate = cuda(p["x"]).clone(), [t.clone() for t in gate_of(p)]
+    x[79:] = float("nan")
+    gate[0][79:] = float("nan")
+    y = torch.full_like(x, 7.0)
+    fwd = kda.gated_scan if entry == "z" else kda.gated_scan_g
+    out = fwd(x, *gate, h0=cuda(p["h0"]), save_states=True, y=y, **how)
+    torch.cuda.synchronize()
+    assert (y[79:] == 7).all()
+    bwd = kda.gated_scan_backward if entry == "z" else kda.gated_scan_g_backward
+    grads = bwd(x, *gate, out[2], cuda(p["dy"]), h0=cuda(p["h0"]), dh_final=cuda(p["dh"]), **how)
+    check(p, out, grads)
+
+
+def test_nothing_leaks_between_sequences():
+    """Infinities and NaN of one sequence and channel stay there; in it they last."""
+    p = make([70, 30, 200, 5], 16, "f32", "z", seed=6)
+    clean_out, clean_grads = run(p)
+    p["x"][80, 3] = float("nan")
+    p["x"][120, 5] = float("inf")
+    p["dy"][85, 7] = float("nan")
+    out, grads = run(p)
+    y = out[0].cpu()
+    assert torch.isnan(y[80:100, 3]).all() and torch.isinf(y[120:300, 5]).all()
+    keep = torch.ones_like(y, dtype=torch.bool)
+    keep[80:100, 3] = keep[100:300, 5] = False
+    assert torch.equal(y[keep], clean_out[0].cpu()[keep])
+    dx = grads[0].cpu()
+    assert torch.isnan(dx[70:86, 7]).all()
+    keep = torch.ones_like(y, dtype=torch.bool)
+    keep[70:100, 7] = False
+    assert torch.equal(dx[keep], clean_grads[0].cpu()[keep])
+
+
+def test_gate_extremes():
+    """z from -inf to +inf: nothing is forgotten, or e^-5 is kept; log-decay -inf clears."""
+    T, C = 130, 8
+    p = make([T], C, "f32", "z", seed=8)
+    p["A"][:] = 0
+    for c, v in enumerate((-300.0, 300.0, -80.0, 80.0, -20.0, 20.0, 0.0, 5.0)):
+        p["z"][:, c] = v
+    check(p, *run(p))
+    p["z"][:, 0], p["z"][:, 1] = -float("inf"), float("inf")
+    out, grads = run(p)
+    assert torch.equal(out[0][:, 0].cpu(), p["h0"][0, 0].expand(T))
+    a = np.exp(-5.0)
+    want = scan.forward(p["x"][:, 1:2], [0, T], g=torch.full((T, 1), -5.0), h0=None)["y"] * (1 - a)
+    want += p["h0"][0, 1].item() * a ** np.arange(1, T + 1)[:, None]
+    close(out[0][:, 1:2], want, 64 * scan.U * (np.abs(want) + 4), "y at z = inf")
+    q = make([100, 40], 16, "f32", "g", seed=9)
+    q["g"][50, ::2] = -float("inf")
+    q["g"][100, :] = -float("inf")
+    q["g"][60, 1] = 0.0
+    check(q, *run(q))
+
+
+def test_long_memory_keeps_its_accuracy():
+    """1 - a near 1e-6 over thousands of tokens: a bias of 1 - a would add up."""
+    p = make([4000], 8, "f32", "z", seed=10)
+    p["A"][:] = 0
+    p["z"][:] = torch.linspace(-16, -8, 8)
+    p["x"][:] = p["x"].abs() + 1
+    p["h0"][:] = 0
+    f = scan.forward(p["x"], [0, 4000], z=p["z"], A=p["A"], h0=p["h0"])
+    out, _ = run(p)
+    # per step: 32 units of its terms; they add up linearly at worst, which the oracle's
+    # bound has; against a value built from 1 - a alone it is at most 32 * 4000 units
+    close(out[0], f["y"], np.minimum(f["e_y"], 32 * 4000 * scan.U * np.abs(f["y"])), "y")
+
+
+def test_repeated_calls_are_bit_identical():
+    for C, lens in ((16, [5000, 3, 700]), (2048, [100, 300]), (264, [4099])):
+        p = make(lens, C, "bf16", "z", seed=C)
+        a, b = run(p), run(p)
+        for s, t in zip((*a[0], *a[1]), (*b[0], *b[1])):
+            if s is not a[0][2]:
+                assert torch.equal(s, t)
+
+
+def test_in_place_state_and_no_final_state():
+    p = make([50, 0, 90], 24, "f32", "z", seed=12)
+    h = cuda(p["h0"]).clone()
+    how = dict(cu_seqlens=cuda(p["cu"]), max_seqlen=90)
+    out, _ = run(p)
+    y, hf = kda.gated_scan(cuda(p["x"]), *gate_of(p), h0=h, h_final=h, **how)
+    assert hf is h and torch.equal(hf, out[1]) and torch.equal(y, out[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,C", [(1, 8), (3, 24), (256, 2048), (5, 1000)])
+def test_step(B, C, dtype):
+    x, z = draw(1, dtype, B, C), draw(2, dtype, B, C, mean=-2.0)
+    A, h = draw(3, "f32", C, std=0.3), draw(4, "f32", B, C)
+    hc = h.cuda()
+    y = kda.gated_scan_step(x.cuda(), z.cuda(), A.cuda(), hc)
+    f = scan.forward(x, list(range(B + 1)), z=z, A=A, h0=h)
+    close(y, f["y"], f["e_y"], "y")
+    close(hc, f["h_final"], f["e_h_final"], "h")
+
+
+def test_steps_continue_a_prefill():
+    """A prefill, then single steps, equals one longer prefill."""
+    N, L, more, C = 4, 37, 5, 48
+    x, z = draw(1, "bf16", N, L + more, C), draw(2, "bf16", N, L + more, C, mean=-3.0)
+    A = draw(3, "f32", C, std=0.3)
+    flat = lambda t, a, b: t[:, a:b].reshape(-1, C).contiguous().cuda()
+    y, h = kda.gated_scan(flat(x, 0, L), flat(z, 0, L), A.cuda(), num_seqs=N)
+    ys = [y.view(N, L, C)]
+    for t in range(L, L + more):
+        ys.append(kda.gated_scan_step(flat(x, t, t + 1), flat(z, t, t + 1), A.cuda(),
+                                      h)[:, None])
+    cu = [n * (L + more) for n in range(N + 1)]
+    f = scan.forward(x.reshape(-1, C), cu, z=z.reshape(-1, C), A=A)
+    close(torch.cat(ys, 1).reshape(-1, C), f["y"], f["e_y"], "y")
+    close(h, f["h_final"], f["e_h_final"], "h")
+
+
+def test_captured_graph_and_side_stream():
+    p = make([300, 200], 24, "bf16", "z", seed=13)
+    want_out, want_grads = run(p)
+    x, gate, h0, dy, dh = (cuda(p["x"]), gate_of(p), cuda(p["h0"]), cuda(p["dy"]), cuda(p["dh"]))
+    how = dict(cu_seqlens=cuda(p["cu"]), max_seqlen=300, h0=h0)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        out = kda.gated_scan(x, *gate, save_states=True, **how)
+        grads = kda.gated_scan_backward(x, *gate, out[2], dy, dh_final=dh, **how)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gout = kda.gated_scan(x, *gate, save_states=True, **how)
+        ggrads = kda.gated_scan_backward(x, *gate, gout[2], dy, dh_final=dh, **how)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for got in ((*out[:2], *grads), (*gout[:2], *ggrads)):
+        for s, t in zip(got, (*want_out[:2], *want_grads)):
+            assert torch.equal(s, t)
+
+
+def test_empty_problem():
+    A = torch.zeros(16, device="cuda")
+    x = torch.zeros(0, 16, device="cuda")
+    h0 = torch.randn(3, 16, device="cuda")
+    cu = torch.zeros(4, dtype=torch.int32, device="cuda")
+    y, h, st = kda.gated_scan(x, x, A, h0=h0, cu_seqlens=cu, max_seqlen=0, save_states=True)
+    assert torch.equal(h, h0) and y.shape == x.shape
+    dx, dz, dA, dh0 = kda.gated_scan_backward(x, x, A, st, x, h0=h0, dh_final=h0, cu_seqlens=cu,
+                                              max_seqlen=0)
+    assert torch.equal(dh0, h0) and (dA == 0).all()
+    y, h = kda.gated_scan_g(x, x, cu_seqlens=cu, max_seqlen=0)
+    assert (h == 0).all()
