@@ -152,7 +152,7 @@ kda_status scan_backward_common(const void* x, const void* z, const float* A, co
   if (T > 0 && (!states || !dy || (z ? !dz : !dg))) return KDA_ERR_INVALID_ARG;
   if (!opt_aligned16(A) || !opt_aligned16(h0) || !opt_aligned16(states) || !opt_aligned16(dy) ||
       !opt_aligned16(dh_final) || !opt_aligned16(dz) || !opt_aligned16(dg) ||
-      !opt_aligned16(dA) || !opt_aligned16(dh0))
+      !opt_aligned16(dA) || !opt_aligned16(dh0) || (dh0 && dh0 == dh_final))
     return KDA_ERR_INVALID_ARG;
   if (N == 0) {
     if (dA && cudaMemsetAsync(dA, 0, (size_t)channels * sizeof(float), (cudaStream_t)stream) !=

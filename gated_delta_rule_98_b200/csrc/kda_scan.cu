@@ -7,9 +7,33 @@
 // Backwards with l_t = dy_t + a_{t+1} l_{t+1}:  dx = (1 - a) l  (z) or l (g),
 // dg = a (h_{t-1} - x) l  (z) or a h_{t-1} l (g).
 //
-// One thread owns one channel of one sequence and walks its tokens; the
-// gradient walks them backwards in spans of 64 and recomputes the states of a
-// span from the state that the forward saved at its start.
+// HBM-bound: every input read once, every output written once.  A run of
+// tokens maps the state entering it to P h + H (P = prod a, H the run from 0),
+// and such maps compose, so tokens are worked on in parallel and only the
+// composition is sequential.  Three levels:
+//  * a thread owns 2 channels of 16 tokens (bf16; fp32: of 8) and runs them
+//    twice, once for (P, H) and once, from the state that enters, for h;
+//  * a warp owns a span of 64 tokens x 16 channels (32 bytes of a bf16 row;
+//    fp32: 8 channels) and composes its 4 (8) runs by shuffles;
+//  * a block owns those channels of the whole token axis (or one of `segments`
+//    parts of it) and its warps take the spans in turn, handing the state from
+//    warp to warp through shared memory and a named barrier per warp.  A warp
+//    needs the state only after it has (P, H), so the hand-over is short and
+//    the loads and the arithmetic of the other warps overlap it.
+// Spans are fetched by cp.async into slots private to a warp, so no barrier
+// joins the block.  With few channels the token axis is cut into segments: a
+// first launch forms each segment's (P, H), reading only what follows the
+// segment's last sequence start, and each block composes those before its own.
+//
+// Sequences are packed along the tokens: a start cuts the composition (P is
+// then negative, and what lies before the cut is not multiplied by 0 but left
+// out, so that an infinity or NaN stays in its sequence).
+//
+// The gradient walks the spans backwards; h_{t-1} is recomputed from the state
+// that the forward saved at every span, in 32 bits, instead of being read back
+// as rounded y (2 bytes an element less to read, and no second rounding).
+#include <type_traits>
+
 #include "kda_common.cuh"
 #include "kda_launch.h"
 
@@ -17,156 +41,795 @@ namespace kda {
 
 namespace {
 
-constexpr int kSpan = 64;  // tokens between saved states (KDA_SCAN_INTERVAL)
-constexpr int kThreads = 64;
-constexpr int kGroups = 64;  // sequences walked at the same time
+constexpr int kSpan = 64;     // tokens of a span, and between saved states (KDA_SCAN_INTERVAL)
+constexpr int kMaxWarps = 15; // one named barrier each (16 in hardware, 0 is __syncthreads)
+constexpr int kMaxSegments = 64;
+constexpr int kRoom = 222 * 1024;  // dynamic shared memory of a block that has an SM to itself
+constexpr float kLog2e = 1.4426950408889634f;
 
-// Token range of sequence n, kept inside [0, T] whatever cu holds.
-__device__ __forceinline__ void tokens_of(const ScanArgs& a, int n, int& t0, int& t1) {
-  seq_bounds(a.cu, n, a.L, t0, t1);
-  t0 = min(max(t0, 0), a.T);
-  t1 = min(max(t1, t0), a.T);
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 neg(float2 x) { return make_float2(-x.x, -x.y); }
+
+__device__ __forceinline__ float2 lds2(const __nv_bfloat16* p) {
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ float2 lds2(const float* p) {
+  return *reinterpret_cast<const float2*>(p);
+}
+__device__ __forceinline__ void stg2(__nv_bfloat16* p, float2 v) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
+__device__ __forceinline__ void stg2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
+
+// a and 1 - a from t = g log2(e) in [-7.3, 0], both to a few units in the last
+// place: t = n + f, 2^f - 1 = f q(f) by its Taylor series (the first term left
+// out is 2e-8 of it at |f| = 1/2), a = 2^n + 2^n f q, 1 - a = (1 - 2^n) - 2^n f q.
+__device__ __forceinline__ void decay(float2 t, float2& a, float2& m) {
+  const float2 magic = splat(12582912.f);  // 1.5 * 2^23: n lands in the low bits
+  const float2 r = __fadd2_rn(t, magic);
+  const float2 f = __fadd2_rn(t, neg(__fadd2_rn(r, neg(magic))));
+  float2 q = splat(1.52527338e-5f);
+  q = __ffma2_rn(q, f, splat(1.54035304e-4f));
+  q = __ffma2_rn(q, f, splat(1.33335581e-3f));
+  q = __ffma2_rn(q, f, splat(9.61812911e-3f));
+  q = __ffma2_rn(q, f, splat(5.55041087e-2f));
+  q = __ffma2_rn(q, f, splat(2.40226507e-1f));
+  q = __ffma2_rn(q, f, splat(6.93147181e-1f));
+  const float2 p = __fmul2_rn(q, f);
+  const float2 s = make_float2(__uint_as_float((__float_as_uint(r.x) << 23) + 0x3f800000u),
+                               __uint_as_float((__float_as_uint(r.y) << 23) + 0x3f800000u));
+  a = __ffma2_rn(s, p, s);
+  m = __ffma2_rn(neg(s), p, __fadd2_rn(splat(1.f), neg(s)));
 }
 
-struct Gate {
-  float a, m, p;  // decay, input scale, s (1 - s) (z only)
+// The library's gate on two channels: k = -e^A log2(e).
+struct GateZ {
+  float2 a, m, p;  // decay, 1 - decay, s (1 - s)
+};
+template <bool kSlope>
+__device__ __forceinline__ GateZ gate_z(float2 z, float2 k) {
+  const float2 u = __fmul2_rn(z, k);
+  const float2 e = make_float2(ex2(u.x), ex2(u.y));  // e^{-e^A z}
+  const float2 d = __fadd2_rn(e, splat(1.f));
+  const float2 s = make_float2(rcp(d.x), rcp(d.y));
+  GateZ g;
+  decay(__fmul2_rn(s, splat(kGateMin * kLog2e)), g.a, g.m);
+  if (kSlope) {
+    // 1 - s = e s: the difference would lose the digits of s near 1.  e = inf gives s = 0.
+    g.p.x = s.x == 0.f ? 0.f : s.x * (s.x * e.x);
+    g.p.y = s.y == 0.f ? 0.f : s.y * (s.y * e.y);
+  }
+  return g;
+}
+
+// Composition of affine maps h -> P h + H; P < 0: a sequence starts inside, H is the state.
+struct Map {
+  float2 P, H;
+};
+__device__ __forceinline__ float then_p(float first, float second) {
+  return second < 0.f ? second : first < 0.f ? first : first * second;
+}
+__device__ __forceinline__ float apply1(float P, float H, float h) {
+  return P < 0.f ? H : fmaf(P, h, H);
+}
+__device__ __forceinline__ float2 apply(const Map& m, float2 h) {
+  return make_float2(apply1(m.P.x, m.H.x, h.x), apply1(m.P.y, m.H.y, h.y));
+}
+__device__ __forceinline__ Map then(const Map& first, const Map& second) {
+  Map r;
+  r.H = apply(second, first.H);
+  r.P = make_float2(then_p(first.P.x, second.P.x), then_p(first.P.y, second.P.y));
+  return r;
+}
+template <bool kUp>
+__device__ __forceinline__ Map shuffle(const Map& m, int lanes) {
+  auto s = [&](float v) {
+    return kUp ? __shfl_up_sync(0xffffffffu, v, lanes) : __shfl_down_sync(0xffffffffu, v, lanes);
+  };
+  Map r;
+  r.P = make_float2(s(m.P.x), s(m.P.y));
+  r.H = make_float2(s(m.H.x), s(m.H.y));
+  return r;
+}
+
+// Tile geometry: rows of 32 bytes of x, 2 channels a lane.
+template <typename T>
+struct Geo {
+  static constexpr int CB = 32 / (int)sizeof(T);  // channels of a block
+  static constexpr int LC = CB / 2;               // lanes along the channels
+  static constexpr int GR = 32 / LC;              // runs of a span
+  static constexpr int K = kSpan / GR;            // tokens of a run
+};
+// Bytes of one tensor's span in shared memory: a spare row after each run moves
+// the runs to different banks, so that a warp's reads do not collide.
+template <typename T, typename E>
+__host__ __device__ constexpr int tile_bytes() {
+  return Geo<T>::GR * (Geo<T>::K + 1) * Geo<T>::CB * (int)sizeof(E);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Rows [t0, t0 + 64) of the block's channels into a tile; zeros outside the tensor.
+template <typename T, typename E>
+__device__ __forceinline__ void fetch(uint32_t tile, const void* src, int64_t t0, int end, int C,
+                                      int c0, int lane) {
+  using G = Geo<T>;
+  constexpr int RB = G::CB * (int)sizeof(E), CH = RB / 16, PER = 16 / (int)sizeof(E);
+#pragma unroll
+  for (int it = 0; it < kSpan * CH / 32; ++it) {
+    const int i = it * 32 + lane, row = i / CH, ch = i % CH;
+    const bool in = t0 + row < end && c0 + ch * PER < C;
+    const char* p = (const char*)src + (in ? ((t0 + row) * C + c0 + ch * PER) * (int64_t)sizeof(E) : 0);
+    copy16(tile + (row + row / G::K) * RB + ch * 16, p, in);
+  }
+}
+
+// The state's way from warp to warp: warp w waits for its turn on barrier 1 + w.
+__device__ __forceinline__ void turn_wait(int w) {
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + w) : "memory");
+}
+__device__ __forceinline__ void turn_pass(int w) {
+  asm volatile("bar.arrive %0, 64;" ::"r"(1 + w) : "memory");
+}
+
+// ------------------------------------------------------------- sequences ----
+
+// Sequence bounds: entry k of cu_seqlens, or k * L; `end` is the end of the last sequence.
+struct Bounds {
+  const int32_t* cu;
+  int N, L, end;
+  __device__ Bounds(const ScanArgs& a) : cu(a.cu), N(a.N), L(a.L) {
+    end = cu ? min(max(cu[N], 0), a.T) : a.T;
+  }
+  __device__ __forceinline__ int64_t at(int k) const { return cu ? cu[k] : (int64_t)k * L; }
+  // First entry in [lo, N] that is >= t (N + 1 if there is none).
+  __device__ __forceinline__ int lower(int lo, int64_t t) const {
+    if (!cu) return L > 0 ? (int)((t + L - 1) / L) : 0;
+    int hi = N + 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (cu[mid] >= t) hi = mid; else lo = mid + 1;
+    }
+    return lo;
+  }
+  // The sequence that holds token t, in [0, N - 1] whatever cu holds.
+  __device__ __forceinline__ int of(int64_t t) const {
+    return min(max(lower(0, t + 1) - 1, 0), N - 1);
+  }
+  __device__ __forceinline__ int up(int n, int64_t t) const {  // of(t) from a lower n
+    while (n < N - 1 && at(n + 1) <= t) ++n;
+    return n;
+  }
+  __device__ __forceinline__ int down(int n, int64_t t) const {  // of(t) from a higher n
+    while (n > 0 && at(n) > t) --n;
+    return n;
+  }
 };
 
-template <typename T, bool kZ>
-__device__ __forceinline__ Gate gate_of(const ScanArgs& a, size_t i, float expA) {
-  if (kZ) {
-    // 1 - s = e s with e = exp(-u): the difference would lose the digits of s near 1
-    const float e = expf(-expA * to_f(((const T*)a.z)[i])), s = 1.f / (1.f + e);
-    const float g = kGateMin * s;
-    return {expf(g), -expm1f(g), s == 0.f ? 0.f : s * (s * e)};
-  }
-  return {expf(a.g[i]), 1.f, 0.f};
-}
-
-template <typename T, bool kZ>
-__global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs a) {
-  const int c = blockIdx.x * kThreads + threadIdx.x;
-  if (c >= a.C) return;
-  const float expA = kZ && a.T > 0 ? expf(a.A[c]) : 0.f;
-  for (int n = blockIdx.y; n < a.N; n += gridDim.y) {
-    int t0, t1;
-  tokens_of(a, n, t0, t1);
-  float h = a.h0 ? a.h0[(size_t)n * a.C + c] : 0.f;
-  for (int t = t0; t < t1; ++t) {
-    const size_t i = (size_t)t * a.C + c;
-    if (a.states && t % kSpan == 0) a.states[(size_t)(t / kSpan) * a.C + c] = h;
-    const Gate u = gate_of<T, kZ>(a, i, expA);
-    h = fmaf(u.a, h, u.m * to_f(((const T*)a.x)[i]));
-    ((T*)a.y)[i] = from_f<T>(h);
-  }
-  if (a.h_final) a.h_final[(size_t)n * a.C + c] = h;
-  }
-}
-
-template <typename T, bool kZ>
-__global__ void __launch_bounds__(kThreads) scan_backward_kernel(const ScanArgs a) {
-  const int c = blockIdx.x * kThreads + threadIdx.x;
-  if (c >= a.C) return;
-  const float expA = kZ && a.T > 0 ? expf(a.A[c]) : 0.f;
-  float dA = 0.f;
-  for (int n = blockIdx.y; n < a.N; n += gridDim.y) {
-    int t0, t1;
-  tokens_of(a, n, t0, t1);
-  float back = a.dh_final ? a.dh_final[(size_t)n * a.C + c] : 0.f;
-  float prev[kSpan];
-  for (int e = t1; e > t0;) {
-    const int b = max((e - 1) / kSpan * kSpan, t0);
-    float h = b == t0 ? (a.h0 ? a.h0[(size_t)n * a.C + c] : 0.f)
-                      : a.states[(size_t)(b / kSpan) * a.C + c];
-    for (int t = b; t < e; ++t) {
-      const size_t i = (size_t)t * a.C + c;
-      const Gate u = gate_of<T, kZ>(a, i, expA);
-      prev[t - b] = h;
-      h = fmaf(u.a, h, u.m * to_f(((const T*)a.x)[i]));
+// Boundaries (sequence starts, and the end) at tokens [t0, t0 + 64]: bit i of
+// `bits` is token t0 + i, `last` is token t0 + 64.
+struct Marks {
+  uint64_t bits;
+  bool last;
+  __device__ __forceinline__ bool any() const { return bits != 0 || last; }
+};
+// A warp's view of the boundaries of the spans it takes, in rising or falling
+// order: `clear` is how far from the last span no boundary lies.
+template <bool kRising>
+struct Marker {
+  int k = 0;
+  int64_t clear = kRising ? -1 : INT64_MAX;
+  __device__ __forceinline__ Marks look(const Bounds& b, int64_t t0, int lane) {
+    Marks m{0, false};
+    if (b.end == t0 + kSpan) m.last = true;
+    else if (b.end < t0 + kSpan) m.bits |= 1ull << (b.end - t0);
+    if (kRising ? clear > t0 + kSpan : clear < t0) return m;
+    k = b.lower(kRising ? min(k, b.N) : 0, t0);
+    if (kRising) clear = k <= b.N ? b.at(k) : INT64_MAX;      // first boundary from t0 on
+    else clear = k <= b.N && b.at(k) == t0 ? t0 : k > 0 ? b.at(k - 1) : -1;  // last one up to t0
+    uint32_t lo = 0, hi = 0, at64 = 0;
+    for (int i = k; i <= b.N; i += 32) {
+      const int64_t v = i + lane <= b.N ? b.at(i + lane) - t0 : INT64_MAX;
+      if (v >= 0 && v < 32) lo |= 1u << v;
+      else if (v >= 32 && v < 64) hi |= 1u << (v - 32);
+      else if (v == 64) at64 = 1;
+      // entries do not fall, so a lane beyond the span ends the search
+      if (__any_sync(0xffffffffu, v > kSpan)) break;
     }
-    for (int t = e - 1; t >= b; --t) {
-      const size_t i = (size_t)t * a.C + c;
-      const Gate u = gate_of<T, kZ>(a, i, expA);
-      const float l = to_f(((const T*)a.dy)[i]) + back;
-      back = u.a * l;
-      ((T*)a.dx)[i] = from_f<T>(u.m * l);
+    lo = __reduce_or_sync(0xffffffffu, lo);
+    hi = __reduce_or_sync(0xffffffffu, hi);
+    m.bits |= (uint64_t)hi << 32 | lo;
+    m.last |= __reduce_or_sync(0xffffffffu, at64) != 0;
+    return m;
+  }
+};
+
+__device__ __forceinline__ float2 row2(const float* p, int n, int C, int c, bool in) {
+  if (!p || !in) return splat(0.f);
+  return *reinterpret_cast<const float2*>(p + (size_t)n * C + c);
+}
+__device__ __forceinline__ void put2(float* p, int n, int C, int c, bool in, float2 v) {
+  if (p && in) *reinterpret_cast<float2*>(p + (size_t)n * C + c) = v;
+}
+
+// What empty sequences hand through (`from`, or zeros) to `to`, for the block's channels.
+__device__ __forceinline__ void pass_empty(const Bounds& b, const float* from, float* to, int C,
+                                           int c0, int CB) {
+  if (!to || (!b.cu && b.L > 0)) return;
+  for (int n = threadIdx.x; n < b.N; n += blockDim.x)
+    if (!b.cu || b.cu[n + 1] <= b.cu[n])
+      for (int c = c0; c < min(c0 + CB, C); c += 2)
+        put2(to, n, C, c, true, row2(from, n, C, c, true));
+}
+
+// ---------------------------------------------------------------- forward ----
+
+// kMaps: form the segment's map (P, H) in `maps` instead of y; else compose
+// the maps of the segments before this one.
+template <typename T, bool kZ, bool kMaps>
+__global__ void __launch_bounds__(kMaxWarps * 32, 1)
+    scan_kernel(const ScanArgs a, int seg_spans, float* maps) {
+  using G = Geo<T>;
+  using E = typename std::conditional<kZ, T, float>::type;
+  constexpr int XB = tile_bytes<T, T>(), STAGE = XB + tile_bytes<T, E>(), D = 3;
+  constexpr int K = G::K, LC = G::LC, GR = G::GR, CB = G::CB;
+  extern __shared__ __align__(16) unsigned char s_raw[];
+  __shared__ float2 s_h[LC], s_p[LC];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+  const int l = lane % LC, grp = lane / LC;
+  const int C = a.C, c0 = blockIdx.x * CB, c = c0 + 2 * l;
+  const bool in = c < C;
+  const Bounds b(a);
+  const int spans = (int)(((int64_t)b.end + kSpan - 1) / kSpan);
+  int j0 = blockIdx.y * seg_spans;
+  const int j1 = min(j0 + seg_spans, spans);
+  if (kMaps) {
+    // the map that later segments need: nothing before the last sequence start matters
+    if (j0 >= j1 || j1 == spans) return;
+    const int64_t te = (int64_t)j1 * kSpan;
+    const int k = b.lower(0, te);
+    if (k <= b.N && b.at(k) == te) {
+      if (warp == 0 && grp == 0) {
+        put2(maps, 2 * blockIdx.y, C, c, in, splat(-1.f));
+        put2(maps, 2 * blockIdx.y + 1, C, c, in, splat(0.f));
+      }
+      return;
+    }
+    if (k > 0) j0 = max(j0, (int)(max(b.at(k - 1), (int64_t)0) / kSpan));
+  } else if (blockIdx.y == 0) {
+    pass_empty(b, a.h0, a.h_final, C, c0, CB);
+  }
+  const uint32_t tiles =
+      (uint32_t)__cvta_generic_to_shared(s_raw) + warp * (D * STAGE);
+  const unsigned char* tiles_p = s_raw + warp * (D * STAGE);
+  const T* X = (const T*)a.x;
+  const E* Z = kZ ? (const E*)a.z : (const E*)a.g;
+  auto request = [&](int j, int slot) {
+    if (j < j1) {
+      fetch<T, T>(tiles + slot * STAGE, X, (int64_t)j * kSpan, b.end, C, c0, lane);
+      fetch<T, E>(tiles + slot * STAGE + XB, Z, (int64_t)j * kSpan, b.end, C, c0, lane);
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < D - 1; ++i) request(j0 + warp + i * W, i);
+  float2 k = splat(0.f);
+  if (kZ && in && b.end > 0) k = make_float2(-kLog2e * expf(a.A[c]), -kLog2e * expf(a.A[c + 1]));
+  Marker<true> marker;
+  int slot = 0;
+  for (int j = j0 + warp; j < j1; j += W) {
+    __syncwarp();
+    request(j + (D - 1) * W, slot == 0 ? D - 1 : slot - 1);
+    copy_wait<D - 1>();
+    __syncwarp();
+    const int64_t t0 = (int64_t)j * kSpan, tk = t0 + grp * K;
+    const T* sx = (const T*)(tiles_p + slot * STAGE) + grp * (K + 1) * CB + 2 * l;
+    const E* sz = (const E*)(tiles_p + slot * STAGE + XB) + grp * (K + 1) * CB + 2 * l;
+    slot = slot == D - 1 ? 0 : slot + 1;
+    const Marks marks = marker.look(b, t0, lane);
+    const bool cut = marks.any();
+    const uint32_t starts = (uint32_t)(marks.bits >> (grp * K)) & ((1u << K) - 1);
+
+    float2 A[K], B[K];
+    Map run{splat(1.f), splat(0.f)};
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const float2 x = lds2(sx + i * CB), z = lds2(sz + i * CB);
       if (kZ) {
-        const float d = back * (prev[t - b] - to_f(((const T*)a.x)[i])) * kGateMin * u.p *
-                        expA;
-        ((T*)a.dz)[i] = from_f<T>(d);
-        dA = fmaf(d, to_f(((const T*)a.z)[i]), dA);
+        const GateZ g = gate_z<false>(z, k);
+        A[i] = g.a;
+        B[i] = __fmul2_rn(g.m, x);
       } else {
-        a.dg[i] = back * prev[t - b];
+        A[i] = make_float2(ex2(z.x * kLog2e), ex2(z.y * kLog2e));
+        B[i] = x;
       }
     }
-    e = b;
+    if (!cut) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        run.H = __ffma2_rn(A[i], run.H, B[i]);
+        run.P = __fmul2_rn(run.P, A[i]);
+      }
+    } else {
+      int n = starts ? b.of(tk) : 0;
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        if (starts >> i & 1) {
+          // B takes the state after the token: the second run must not read h0 again,
+          // which may be h_final and by then hold a sequence's end
+          n = b.up(n, tk + i);
+          B[i] = __ffma2_rn(A[i], row2(a.h0, n, C, c, in && tk + i < b.end), B[i]);
+          run.H = B[i];
+          run.P = splat(-1.f);
+        } else {
+          run.H = __ffma2_rn(A[i], run.H, B[i]);
+        }
+        run.P = make_float2(run.P.x < 0.f ? -1.f : run.P.x * A[i].x,
+                            run.P.y < 0.f ? -1.f : run.P.y * A[i].y);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < GR; o <<= 1) {
+      const Map before = shuffle<true>(run, o * LC);
+      if (grp >= o) run = then(before, run);
+    }
+    Map before = shuffle<true>(run, LC);
+    if (grp == 0) before = Map{splat(1.f), splat(0.f)};
+
+    // the state (and, for a segment's map, the product) before this span
+    float2 h_in = splat(0.f), p_in = splat(1.f);
+    if (j > j0) {
+      if (W > 1) turn_wait(warp);
+      h_in = s_h[l];
+      if (kMaps) p_in = s_p[l];
+    } else if (!kMaps) {
+      for (int s = 0; s < (int)blockIdx.y; ++s)
+        h_in = apply(Map{row2(maps, 2 * s, C, c, in), row2(maps, 2 * s + 1, C, c, in)}, h_in);
+    }
+    __syncwarp();
+    const float2 h_out = apply(run, h_in);
+    float2 p_out = p_in;
+    if (kMaps) p_out = make_float2(then_p(p_in.x, run.P.x), then_p(p_in.y, run.P.y));
+    if (grp == GR - 1) {
+      s_h[l] = h_out;
+      if (kMaps) s_p[l] = p_out;
+      if (kMaps && j == j1 - 1) {
+        put2(maps, 2 * blockIdx.y, C, c, in, p_out);
+        put2(maps, 2 * blockIdx.y + 1, C, c, in, h_out);
+      }
+    }
+    __syncwarp();
+    if (j + 1 < j1 && W > 1) turn_pass(warp + 1 == W ? 0 : warp + 1);
+    if (kMaps) continue;
+
+    if (grp == 0) put2(a.states, j, C, c, in, h_in);
+    float2 h = apply(before, h_in);
+    T* y = (T*)a.y + tk * C + c;
+    if (!cut) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        h = __ffma2_rn(A[i], h, B[i]);
+        if (in) stg2(y + (int64_t)i * C, h);
+      }
+    } else {
+      const uint32_t ends = (uint32_t)((marks.bits >> 1 | (uint64_t)marks.last << 63) >> (grp * K)) &
+                            ((1u << K) - 1);
+      int n = (starts | ends) ? b.of(tk) : 0;
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        const bool live = in && tk + i < b.end;
+        if (starts >> i & 1) {
+          n = b.up(n, tk + i);
+          h = B[i];
+        } else {
+          h = __ffma2_rn(A[i], h, B[i]);
+        }
+        if (live) {
+          stg2(y + (int64_t)i * C, h);
+          if (ends >> i & 1) put2(a.h_final, n, C, c, true, h);
+        }
+      }
+    }
   }
-  if (a.dh0) a.dh0[(size_t)n * a.C + c] = back;
-  }
-  if (kZ) ((float*)a.ws)[(size_t)blockIdx.y * a.C + c] = dA;
+  copy_wait<0>();
 }
 
-__global__ void __launch_bounds__(kThreads)
+// --------------------------------------------------------------- backward ----
+
+// kMaps: form the map of the gradient through the segment, from its last token
+// to its first, in `maps`; else compose the maps of the segments after this
+// one.  dA of the segment's tokens goes to row blockIdx.y of dA_part.
+template <typename T, bool kZ, bool kMaps>
+__global__ void __launch_bounds__(kMaxWarps * 32, 1)
+    scan_backward_kernel(const ScanArgs a, int seg_spans, float* maps, float* dA_part) {
+  using G = Geo<T>;
+  using E = typename std::conditional<kZ, T, float>::type;
+  constexpr int XB = tile_bytes<T, T>(), ZB = tile_bytes<T, E>(), STAGE = 2 * XB + ZB, D = 2;
+  constexpr int K = G::K, LC = G::LC, GR = G::GR, CB = G::CB;
+  extern __shared__ __align__(16) unsigned char s_raw[];
+  __shared__ float2 s_h[LC], s_p[LC], s_dA[kMaxWarps][LC];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+  const int l = lane % LC, grp = lane / LC;
+  const int C = a.C, c0 = blockIdx.x * CB, c = c0 + 2 * l;
+  const bool in = c < C;
+  const Bounds b(a);
+  const int spans = (int)(((int64_t)b.end + kSpan - 1) / kSpan);
+  const int j0 = blockIdx.y * seg_spans;
+  int j1 = min(j0 + seg_spans, spans);
+  if (kMaps) {
+    // the map that earlier segments need: nothing after the first sequence end matters
+    if (j0 >= j1 || j0 == 0) return;
+    const int64_t ts = (int64_t)j0 * kSpan;
+    const int k = b.lower(0, ts);
+    if (k <= b.N && b.at(k) == ts) {
+      if (warp == 0 && grp == 0) {
+        put2(maps, 2 * blockIdx.y, C, c, in, splat(-1.f));
+        put2(maps, 2 * blockIdx.y + 1, C, c, in, splat(0.f));
+      }
+      return;
+    }
+    if (k <= b.N) {
+      const int64_t e = min(b.at(k), (int64_t)b.end);
+      j1 = min(j1, (int)((e + kSpan - 1) / kSpan));
+    }
+  } else if (blockIdx.y == 0) {
+    pass_empty(b, a.dh_final, a.dh0, C, c0, CB);
+  }
+  const uint32_t tiles = (uint32_t)__cvta_generic_to_shared(s_raw) + warp * (D * STAGE);
+  const unsigned char* tiles_p = s_raw + warp * (D * STAGE);
+  const E* Z = kZ ? (const E*)a.z : (const E*)a.g;
+  auto request = [&](int j, int slot) {
+    if (j >= j0) {
+      const int64_t t0 = (int64_t)j * kSpan;
+      if (!kMaps) fetch<T, T>(tiles + slot * STAGE, a.x, t0, b.end, C, c0, lane);
+      fetch<T, T>(tiles + slot * STAGE + XB, a.dy, t0, b.end, C, c0, lane);
+      fetch<T, E>(tiles + slot * STAGE + 2 * XB, Z, t0, b.end, C, c0, lane);
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < D - 1; ++i) request(j1 - 1 - warp - i * W, i);
+  float2 k = splat(0.f);
+  if (kZ && in && b.end > 0) k = make_float2(-kLog2e * expf(a.A[c]), -kLog2e * expf(a.A[c + 1]));
+  // -5 e^A, the constant factors of dz
+  const float2 kz = __fmul2_rn(k, splat(-kGateMin / kLog2e));
+  float2 dA = splat(0.f);
+  Marker<false> marker;
+  int slot = 0;
+  for (int j = j1 - 1 - warp; j >= j0; j -= W) {
+    __syncwarp();
+    request(j - (D - 1) * W, slot == 0 ? D - 1 : slot - 1);
+    const float2 state = kMaps ? splat(0.f) : row2(a.states, j, C, c, in);
+    copy_wait<D - 1>();
+    __syncwarp();
+    const int64_t t0 = (int64_t)j * kSpan, tk = t0 + grp * K;
+    const unsigned char* tile = tiles_p + slot * STAGE;
+    const int off = grp * (K + 1) * CB + 2 * l;
+    const T* sx = (const T*)tile + off;
+    const T* sd = (const T*)(tile + XB) + off;
+    const E* sz = (const E*)(tile + 2 * XB) + off;
+    slot = slot == D - 1 ? 0 : slot + 1;
+    const Marks marks = marker.look(b, t0, lane);
+    const bool cut = marks.any();
+    const uint32_t starts = (uint32_t)(marks.bits >> (grp * K)) & ((1u << K) - 1);
+    const uint32_t ends =
+        (uint32_t)((marks.bits >> 1 | (uint64_t)marks.last << 63) >> (grp * K)) & ((1u << K) - 1);
+
+    // fwd: the state through the run; bwd: the gradient that leaves its first token,
+    // for the gradient entering behind its last one
+    float2 A[K], H[K];
+    Map fwd{splat(1.f), splat(0.f)}, bwd{splat(1.f), splat(0.f)};
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const float2 z = lds2(sz + i * CB);
+      if (kZ) {
+        const GateZ g = gate_z<false>(z, k);
+        A[i] = g.a;
+        if (!kMaps) H[i] = __fmul2_rn(g.m, lds2(sx + i * CB));
+      } else {
+        A[i] = make_float2(ex2(z.x * kLog2e), ex2(z.y * kLog2e));
+        if (!kMaps) H[i] = lds2(sx + i * CB);
+      }
+    }
+    int n_first = 0;
+    if (!cut) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        if (!kMaps) fwd.H = __ffma2_rn(A[i], fwd.H, H[i]);
+        bwd.P = __fmul2_rn(bwd.P, A[i]);
+        bwd.H = __ffma2_rn(bwd.P, lds2(sd + i * CB), bwd.H);
+      }
+      fwd.P = bwd.P;
+    } else {
+      n_first = (starts | ends) ? b.of(tk) : 0;
+      int n = n_first;
+      float2 P = splat(1.f);  // product up to the run's first sequence end
+      bool open = true;
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        const bool live = in && tk + i < b.end;
+        if (starts >> i & 1) {
+          n = b.up(n, tk + i);
+          fwd.H = row2(a.h0, n, C, c, live);
+          fwd.P = splat(-1.f);
+        }
+        if (!kMaps) {
+          fwd.H = __ffma2_rn(A[i], fwd.H, H[i]);
+          fwd.P = make_float2(fwd.P.x < 0.f ? -1.f : fwd.P.x * A[i].x,
+                              fwd.P.y < 0.f ? -1.f : fwd.P.y * A[i].y);
+        }
+        if (open) {
+          P = __fmul2_rn(P, A[i]);
+          float2 d = lds2(sd + i * CB);
+          if (ends >> i & 1) d = __fadd2_rn(d, row2(a.dh_final, n, C, c, live));
+          bwd.H = __ffma2_rn(P, d, bwd.H);
+          if (ends >> i & 1) open = false;
+        }
+      }
+      bwd.P = open ? P : splat(-1.f);
+    }
+    Map before{splat(1.f), splat(0.f)};
+    if (!kMaps) {
+#pragma unroll
+      for (int o = 1; o < GR; o <<= 1) {
+        const Map m = shuffle<true>(fwd, o * LC);
+        if (grp >= o) fwd = then(m, fwd);
+      }
+      before = shuffle<true>(fwd, LC);
+      if (grp == 0) before = Map{splat(1.f), splat(0.f)};
+    }
+#pragma unroll
+    for (int o = 1; o < GR; o <<= 1) {
+      const Map m = shuffle<false>(bwd, o * LC);
+      if (grp + o < GR) bwd = then(m, bwd);
+    }
+    Map after = shuffle<false>(bwd, LC);
+    if (grp == GR - 1) after = Map{splat(1.f), splat(0.f)};
+
+    float2 l_in = splat(0.f), p_in = splat(1.f);
+    if (j < j1 - 1) {
+      if (W > 1) turn_wait(warp);
+      l_in = s_h[l];
+      if (kMaps) p_in = s_p[l];
+    } else if (!kMaps) {
+      const int last = (spans + seg_spans - 1) / seg_spans - 1;
+      for (int s = last; s > (int)blockIdx.y; --s)
+        l_in = apply(Map{row2(maps, 2 * s, C, c, in), row2(maps, 2 * s + 1, C, c, in)}, l_in);
+    }
+    __syncwarp();
+    const float2 l_out = apply(bwd, l_in);
+    float2 p_out = p_in;
+    if (kMaps) p_out = make_float2(then_p(p_in.x, bwd.P.x), then_p(p_in.y, bwd.P.y));
+    if (grp == 0) {
+      s_h[l] = l_out;
+      if (kMaps) s_p[l] = p_out;
+      if (kMaps && j == j0) {
+        put2(maps, 2 * blockIdx.y, C, c, in, p_out);
+        put2(maps, 2 * blockIdx.y + 1, C, c, in, l_out);
+      }
+    }
+    __syncwarp();
+    if (j > j0 && W > 1) turn_pass(warp + 1 == W ? 0 : warp + 1);
+    if (kMaps) continue;
+
+    // the state before each token, in place of the token's input
+    float2 h = apply(before, state), back = apply(after, l_in), dA_span = splat(0.f);
+    int n = n_first;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      if (cut && (starts >> i & 1)) {
+        n = b.up(n, tk + i);
+        h = row2(a.h0, n, C, c, in && tk + i < b.end);
+      }
+      const float2 now = h;
+      h = __ffma2_rn(A[i], h, H[i]);
+      H[i] = now;
+    }
+    const int64_t at = tk * C + c;
+#pragma unroll
+    for (int i = K - 1; i >= 0; --i) {
+      const bool live = in && (!cut || tk + i < b.end);
+      if (cut && (ends >> i & 1)) {
+        n = b.down(n, tk + i);
+        back = row2(a.dh_final, n, C, c, live);
+      }
+      const float2 lam = __fadd2_rn(lds2(sd + i * CB), back);
+      back = __fmul2_rn(A[i], lam);
+      if (kZ) {
+        const float2 z = lds2(sz + i * CB);
+        const GateZ g = gate_z<true>(z, k);
+        const float2 d = __fadd2_rn(H[i], neg(lds2(sx + i * CB)));
+        const float2 dz = __fmul2_rn(__fmul2_rn(back, d), __fmul2_rn(g.p, kz));
+        if (live) {
+          stg2((T*)a.dx + at + (int64_t)i * C, __fmul2_rn(g.m, lam));
+          stg2((T*)a.dz + at + (int64_t)i * C, dz);
+          dA_span = __ffma2_rn(dz, z, dA_span);
+        }
+      } else if (live) {
+        stg2((T*)a.dx + at + (int64_t)i * C, lam);
+        stg2(a.dg + at + (int64_t)i * C, __fmul2_rn(back, H[i]));
+      }
+      if (cut && (starts >> i & 1)) {
+        n = b.down(n, tk + i);
+        put2(a.dh0, n, C, c, live, back);
+      }
+    }
+    dA = __fadd2_rn(dA, dA_span);
+  }
+  copy_wait<0>();
+  if (kZ && !kMaps) {
+    // over the runs, then over the warps, in a fixed order
+#pragma unroll
+    for (int o = LC; o < 32; o <<= 1) {
+      dA.x += __shfl_xor_sync(0xffffffffu, dA.x, o);
+      dA.y += __shfl_xor_sync(0xffffffffu, dA.y, o);
+    }
+    if (grp == 0) s_dA[warp][l] = dA;
+    __syncthreads();
+    if (warp == 0 && grp == 0) {
+      float2 v = s_dA[0][l];
+      for (int w = 1; w < W; ++w) v = __fadd2_rn(v, s_dA[w][l]);
+      put2(dA_part, blockIdx.y, C, c, in, v);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(64)
     sum_rows_kernel(const float* part, int rows, int C, float* out) {
-  const int c = blockIdx.x * kThreads + threadIdx.x;
+  const int c = blockIdx.x * 64 + threadIdx.x;
   if (c >= C) return;
   float s = 0.f;
   for (int n = 0; n < rows; ++n) s += part[(size_t)n * C + c];
   out[c] = s;
 }
 
+// ------------------------------------------------------------------- step ----
+
 template <typename T>
 __global__ void __launch_bounds__(256)
     step_kernel(const T* x, const T* z, const float* A, float* h, size_t count, int C, T* y) {
-  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (size_t)gridDim.x * 256) {
-    const float g = gate_logdecay(to_f(z[i]), expf(A[i % C]));
-    const float v = fmaf(expf(g), h[i], -expm1f(g) * to_f(x[i]));
-    h[i] = v;
-    y[i] = from_f<T>(v);
+  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 2;
+  if (i >= count) return;
+  const int c = (int)(i % C);
+  const float2 a = *reinterpret_cast<const float2*>(A + c);
+  const float2 xv = lds2(x + i), zv = lds2(z + i), hv = lds2(h + i);
+  const GateZ g = gate_z<false>(zv, make_float2(-kLog2e * expf(a.x), -kLog2e * expf(a.y)));
+  const float2 v = __ffma2_rn(g.a, hv, __fmul2_rn(g.m, xv));
+  stg2(h + i, v);
+  stg2(y + i, v);
+}
+
+// ----------------------------------------------------------------- launch ----
+
+// Segments of the token axis: one block per SM and channel group at least,
+// segments of 16 spans at least.
+int segments(int T, int cols) {
+  const int spans = (int)(((int64_t)T + kSpan - 1) / kSpan);
+  if (cols >= 100) return 1;
+  int s = 296 / cols;
+  s = s < spans / 16 ? s : spans / 16;
+  return s < 1 ? 1 : s > kMaxSegments ? kMaxSegments : s;
+}
+
+struct Plan {
+  int cols, segs, seg_spans, warps, smem;
+};
+// Warps and shared memory: one block of up to 15 warps on an SM, or two of 8
+// when there are more blocks than SMs.
+Plan plan(const ScanArgs& a, int CB, int slot_bytes, bool one_segment) {
+  Plan p;
+  p.cols = (a.C + CB - 1) / CB;
+  p.segs = one_segment ? 1 : segments(a.T, p.cols);
+  const int spans = (int)(((int64_t)a.T + kSpan - 1) / kSpan);
+  p.seg_spans = (spans + p.segs - 1) / p.segs;
+  if (p.seg_spans < 1) p.seg_spans = 1;
+  p.segs = spans > 0 ? (spans + p.seg_spans - 1) / p.seg_spans : 1;
+  const bool two = (int64_t)p.cols * p.segs > 148;
+  const int room = two ? kRoom / 2 - 1024 : kRoom, most = two ? 8 : kMaxWarps;
+  p.warps = room / slot_bytes < most ? room / slot_bytes : most;
+  if (p.warps > p.seg_spans) p.warps = p.seg_spans;
+  p.smem = p.warps * slot_bytes;
+  return p;
+}
+
+// The same bound at every call, so that calls from several threads agree.
+template <typename F>
+cudaError_t allow(F* kernel) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
+}
+
+template <typename T, bool kZ>
+cudaError_t forward_t(const ScanArgs& a) {
+  using E = typename std::conditional<kZ, T, float>::type;
+  const int slot = 3 * (tile_bytes<T, T>() + tile_bytes<T, E>());
+  // a later segment writes h_final while an earlier one reads h0: not in place
+  const Plan p = plan(a, Geo<T>::CB, slot, a.h0 && a.h0 == a.h_final);
+  float* maps = (float*)a.ws;
+  const dim3 grid(p.cols, p.segs);
+  cudaError_t err = allow(scan_kernel<T, kZ, false>);
+  if (err != cudaSuccess) return err;
+  if (p.segs > 1) {
+    if ((err = allow(scan_kernel<T, kZ, true>)) != cudaSuccess) return err;
+    scan_kernel<T, kZ, true><<<grid, p.warps * 32, p.smem, a.stream>>>(a, p.seg_spans, maps);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
   }
+  scan_kernel<T, kZ, false><<<grid, p.warps * 32, p.smem, a.stream>>>(a, p.seg_spans, maps);
+  return cudaGetLastError();
+}
+
+template <typename T, bool kZ>
+cudaError_t backward_t(const ScanArgs& a) {
+  using E = typename std::conditional<kZ, T, float>::type;
+  const int slot = 2 * (2 * tile_bytes<T, T>() + tile_bytes<T, E>());
+  const Plan p = plan(a, Geo<T>::CB, slot, false);
+  float* maps = (float*)a.ws;
+  float* part = p.segs > 1 ? maps + (size_t)2 * p.segs * a.C : a.dA;
+  const dim3 grid(p.cols, p.segs);
+  cudaError_t err = allow(scan_backward_kernel<T, kZ, false>);
+  if (err != cudaSuccess) return err;
+  if (p.segs > 1) {
+    if ((err = allow(scan_backward_kernel<T, kZ, true>)) != cudaSuccess) return err;
+    scan_backward_kernel<T, kZ, true>
+        <<<grid, p.warps * 32, p.smem, a.stream>>>(a, p.seg_spans, maps, nullptr);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  }
+  scan_backward_kernel<T, kZ, false>
+      <<<grid, p.warps * 32, p.smem, a.stream>>>(a, p.seg_spans, maps, part);
+  if ((err = cudaGetLastError()) != cudaSuccess || !kZ || p.segs == 1) return err;
+  sum_rows_kernel<<<(a.C + 63) / 64, 64, 0, a.stream>>>(part, p.segs, a.C, a.dA);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t scan_workspace_bytes(int T, int C) { return (size_t)kGroups * C * sizeof(float); }
+size_t scan_workspace_bytes(int T, int C) {
+  const int wide = segments(T, (C + Geo<__nv_bfloat16>::CB - 1) / Geo<__nv_bfloat16>::CB);
+  const int narrow = segments(T, (C + Geo<float>::CB - 1) / Geo<float>::CB);
+  return (size_t)3 * (wide > narrow ? wide : narrow) * C * sizeof(float);
+}
 
 cudaError_t launch_scan(const ScanArgs& a) {
-  const dim3 grid((a.C + kThreads - 1) / kThreads, min(a.N, kGroups));
-  if (a.g) {
-    if (a.bf16) scan_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, a.stream>>>(a);
-    else scan_kernel<float, false><<<grid, kThreads, 0, a.stream>>>(a);
-  } else {
-    if (a.bf16) scan_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, a.stream>>>(a);
-    else scan_kernel<float, true><<<grid, kThreads, 0, a.stream>>>(a);
-  }
-  return cudaGetLastError();
+  if (a.g || !a.z) return a.bf16 ? forward_t<__nv_bfloat16, false>(a) : forward_t<float, false>(a);
+  return a.bf16 ? forward_t<__nv_bfloat16, true>(a) : forward_t<float, true>(a);
 }
 
 cudaError_t launch_scan_backward(const ScanArgs& a) {
-  const dim3 grid((a.C + kThreads - 1) / kThreads, min(a.N, kGroups));
-  if (!a.dA) {
-    if (a.bf16) scan_backward_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, a.stream>>>(a);
-    else scan_backward_kernel<float, false><<<grid, kThreads, 0, a.stream>>>(a);
-    return cudaGetLastError();
-  }
-  if (a.bf16) scan_backward_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, a.stream>>>(a);
-  else scan_backward_kernel<float, true><<<grid, kThreads, 0, a.stream>>>(a);
-  cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  sum_rows_kernel<<<grid.x, kThreads, 0, a.stream>>>((const float*)a.ws, grid.y, a.C, a.dA);
-  return cudaGetLastError();
+  if (!a.dA)
+    return a.bf16 ? backward_t<__nv_bfloat16, false>(a) : backward_t<float, false>(a);
+  return a.bf16 ? backward_t<__nv_bfloat16, true>(a) : backward_t<float, true>(a);
 }
 
 cudaError_t launch_scan_step(const void* x, const void* z, const float* A, float* h, int B, int C,
                              bool bf16, void* y, cudaStream_t stream) {
   const size_t count = (size_t)B * C;
-  const int grid = (int)(count / 256 < 148 * 8 ? (count + 255) / 256 : 148 * 8);
+  const size_t grid = (count / 2 + 255) / 256;
+  if (grid > 0x7fffffffu) return cudaErrorInvalidValue;
   if (bf16)
-    step_kernel<<<grid, 256, 0, stream>>>((const __nv_bfloat16*)x, (const __nv_bfloat16*)z, A, h,
-                                          count, C, (__nv_bfloat16*)y);
+    step_kernel<<<(unsigned)grid, 256, 0, stream>>>((const __nv_bfloat16*)x,
+                                                    (const __nv_bfloat16*)z, A, h, count, C,
+                                                    (__nv_bfloat16*)y);
   else
-    step_kernel<<<grid, 256, 0, stream>>>((const float*)x, (const float*)z, A, h, count, C,
-                                          (float*)y);
+    step_kernel<<<(unsigned)grid, 256, 0, stream>>>((const float*)x, (const float*)z, A, h, count,
+                                                    C, (float*)y);
   return cudaGetLastError();
 }
 

@@ -458,8 +458,8 @@ kda_status kda_gated_scan_g(const void* x, const float* g, const float* h0,
  *             by) the forward call; h_{t-1} is recomputed from the states.
  *  dy       : [T, channels] in `dt`;  dh_final : [N, channels] float32 or NULL (zeros).
  *  dx, dz   : [T, channels] in `dt`;  dA : [channels] float32, overwritten;
- *  dh0      : [N, channels] float32 or NULL (not wanted); may equal dh_final.
- *             Outputs must not overlap the other inputs.  Rows from
+ *  dh0      : [N, channels] float32 or NULL (not wanted).
+ *             Outputs must not overlap any input.  Rows from
  *             cu_seqlens[N] on keep what they held.
  *  workspace: kda_gated_scan_workspace_size bytes.
  */
