@@ -113,6 +113,8 @@ kda_status check_scan(const void* x, const void* gate, const int32_t* cu, int32_
   if (dt != KDA_F32 && dt != KDA_BF16) return KDA_ERR_UNSUPPORTED;
   if (channels < 8 || channels % 8 != 0) return KDA_ERR_UNSUPPORTED;
   if (N < 0 || T < 0 || max_len < 0) return KDA_ERR_INVALID_ARG;
+  // the kernels' token and row-pitch arithmetic is 32-bit (offsets are 64-bit)
+  if (T > 0x7fffff00 || channels > (1 << 28)) return KDA_ERR_UNSUPPORTED;
   if (!cu && (int64_t)N * max_len != T) return KDA_ERR_INVALID_ARG;
   if (N == 0 && T > 0) return KDA_ERR_INVALID_ARG;
   if (!opt_aligned4(cu)) return KDA_ERR_INVALID_ARG;

@@ -42,7 +42,7 @@ namespace kda {
 namespace {
 
 constexpr int kSpan = 64;     // tokens of a span, and between saved states (KDA_SCAN_INTERVAL)
-constexpr int kMaxWarps = 15; // one named barrier each (16 in hardware, 0 is __syncthreads)
+constexpr int kMaxWarps = 12; // 168 registers a thread; at most 15 (a named barrier each)
 constexpr int kMaxSegments = 64;
 constexpr int kRoom = 222 * 1024;  // dynamic shared memory of a block that has an SM to itself
 constexpr float kLog2e = 1.4426950408889634f;
@@ -58,7 +58,6 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 __device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 neg(float2 x) { return make_float2(-x.x, -x.y); }
 
 __device__ __forceinline__ float2 lds2(const __nv_bfloat16* p) {
   const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
@@ -73,24 +72,26 @@ __device__ __forceinline__ void stg2(__nv_bfloat16* p, float2 v) {
 __device__ __forceinline__ void stg2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
 
 // a and 1 - a from t = g log2(e) in [-7.3, 0], both to a few units in the last
-// place: t = n + f, 2^f - 1 = f q(f) by its Taylor series (the first term left
-// out is 2e-8 of it at |f| = 1/2), a = 2^n + 2^n f q, 1 - a = (1 - 2^n) - 2^n f q.
+// place: t = n + f, 2^f - 1 = f q(f) with q interpolated at the 6 Chebyshev nodes
+// of |f| <= 1/2 (2e-8 of it at most), a = 2^n + 2^n f q, 1 - a = (1 - 2^n) - 2^n f q.
+// Without the special function unit, which the sigmoid keeps busy.
 __device__ __forceinline__ void decay(float2 t, float2& a, float2& m) {
   const float2 magic = splat(12582912.f);  // 1.5 * 2^23: n lands in the low bits
   const float2 r = __fadd2_rn(t, magic);
-  const float2 f = __fadd2_rn(t, neg(__fadd2_rn(r, neg(magic))));
-  float2 q = splat(1.52527338e-5f);
-  q = __ffma2_rn(q, f, splat(1.54035304e-4f));
-  q = __ffma2_rn(q, f, splat(1.33335581e-3f));
-  q = __ffma2_rn(q, f, splat(9.61812911e-3f));
-  q = __ffma2_rn(q, f, splat(5.55041087e-2f));
+  const float2 f = __fadd2_rn(t, __ffma2_rn(r, splat(-1.f), magic));
+  float2 q = splat(1.54531634e-4f);
+  q = __ffma2_rn(q, f, splat(1.33908633e-3f));
+  q = __ffma2_rn(q, f, splat(9.61808302e-3f));
+  q = __ffma2_rn(q, f, splat(5.55035695e-2f));
   q = __ffma2_rn(q, f, splat(2.40226507e-1f));
-  q = __ffma2_rn(q, f, splat(6.93147181e-1f));
+  q = __ffma2_rn(q, f, splat(6.93147182e-1f));
   const float2 p = __fmul2_rn(q, f);
-  const float2 s = make_float2(__uint_as_float((__float_as_uint(r.x) << 23) + 0x3f800000u),
-                               __uint_as_float((__float_as_uint(r.y) << 23) + 0x3f800000u));
+  const uint32_t x = __float_as_uint(r.x) << 23, y = __float_as_uint(r.y) << 23;
+  const float2 s = make_float2(__uint_as_float(x + 0x3f800000u), __uint_as_float(y + 0x3f800000u));
+  const float2 ns =
+      make_float2(__uint_as_float(x + 0xbf800000u), __uint_as_float(y + 0xbf800000u));
   a = __ffma2_rn(s, p, s);
-  m = __ffma2_rn(neg(s), p, __fadd2_rn(splat(1.f), neg(s)));
+  m = __ffma2_rn(ns, p, __fadd2_rn(ns, splat(1.f)));
 }
 
 // The library's gate on two channels: k = -e^A log2(e).
@@ -132,6 +133,10 @@ __device__ __forceinline__ Map then(const Map& first, const Map& second) {
   r.P = make_float2(then_p(first.P.x, second.P.x), then_p(first.P.y, second.P.y));
   return r;
 }
+// Without a sequence start in either.
+__device__ __forceinline__ Map then_plain(const Map& first, const Map& second) {
+  return Map{__fmul2_rn(first.P, second.P), __ffma2_rn(second.P, first.H, second.H)};
+}
 template <bool kUp>
 __device__ __forceinline__ Map shuffle(const Map& m, int lanes) {
   auto s = [&](float v) {
@@ -141,6 +146,21 @@ __device__ __forceinline__ Map shuffle(const Map& m, int lanes) {
   r.P = make_float2(s(m.P.x), s(m.P.y));
   r.H = make_float2(s(m.H.x), s(m.H.y));
   return r;
+}
+
+// Composes the maps of a span's GR runs (LC lanes each), in rising order of the
+// runs or falling: `run` becomes the map up to and with the lane's run, the
+// result is the map up to it.  kPlain: no sequence starts inside.
+template <int LC, bool kUp, bool kPlain>
+__device__ __forceinline__ Map compose(Map& run, int lane) {
+  const int at = kUp ? lane : 31 - lane;
+#pragma unroll
+  for (int o = LC; o < 32; o <<= 1) {
+    const Map m = shuffle<kUp>(run, o);
+    if (at >= o) run = kPlain ? then_plain(m, run) : then(m, run);
+  }
+  const Map before = shuffle<kUp>(run, LC);
+  return at < LC ? Map{splat(1.f), splat(0.f)} : before;
 }
 
 // Tile geometry: rows of 32 bytes of x, 2 channels a lane.
@@ -168,20 +188,39 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// Rows [t0, t0 + 64) of the block's channels into a tile; zeros outside the tensor.
+// One tensor's way into a warp's slots: lane `lane` brings 16 bytes of a row, a
+// span takes kSpan * CH / 32 copies of 32 / CH rows each.
 template <typename T, typename E>
-__device__ __forceinline__ void fetch(uint32_t tile, const void* src, int64_t t0, int end, int C,
-                                      int c0, int lane) {
-  using G = Geo<T>;
-  constexpr int RB = G::CB * (int)sizeof(E), CH = RB / 16, PER = 16 / (int)sizeof(E);
-#pragma unroll
-  for (int it = 0; it < kSpan * CH / 32; ++it) {
-    const int i = it * 32 + lane, row = i / CH, ch = i % CH;
-    const bool in = t0 + row < end && c0 + ch * PER < C;
-    const char* p = (const char*)src + (in ? ((t0 + row) * C + c0 + ch * PER) * (int64_t)sizeof(E) : 0);
-    copy16(tile + (row + row / G::K) * RB + ch * 16, p, in);
+struct Source {
+  static constexpr int RB = Geo<T>::CB * (int)sizeof(E), CH = RB / 16, PER = 16 / (int)sizeof(E);
+  static constexpr int ROWS = 32 / CH, COPIES = kSpan / ROWS;
+  const char* base;
+  const char* p;   // this lane's piece of the first copy's row of span 0
+  int row, pitch;  // the row in that copy; bytes of a row of the tensor
+  uint32_t dst;    // the piece's place in a slot
+  bool in;         // the piece is in the tensor
+  __device__ Source(const void* src, int C, int c0, int lane) {
+    const int ch = lane % CH;
+    base = (const char*)src;
+    row = lane / CH;
+    pitch = C * (int)sizeof(E);
+    in = c0 + ch * PER < C;
+    p = (const char*)src + (int64_t)row * pitch + (int64_t)(in ? c0 + ch * PER : 0) * sizeof(E);
+    dst = (row + row / Geo<T>::K) * RB + ch * 16;
   }
-}
+  // Span j into the tile; zeros outside the tensor and from token `end` on.
+  __device__ __forceinline__ void fetch(uint32_t tile, int j, int end) const {
+    const char* q = p + (int64_t)j * kSpan * pitch;
+    const int left = end - j * kSpan - row;  // rows from this lane's first one to the end
+#pragma unroll
+    for (int it = 0; it < COPIES; ++it) {
+      static_assert(ROWS % Geo<T>::K == 0 || Geo<T>::K % ROWS == 0, "spare rows");
+      const bool live = in && it * ROWS < left;
+      copy16(tile + dst + (it * ROWS + it * ROWS / Geo<T>::K) * RB,
+             live ? q + (int64_t)(it * ROWS) * pitch : base, live);
+    }
+  }
+};
 
 // The state's way from warp to warp: warp w waits for its turn on barrier 1 + w.
 __device__ __forceinline__ void turn_wait(int w) {
@@ -321,12 +360,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   const uint32_t tiles =
       (uint32_t)__cvta_generic_to_shared(s_raw) + warp * (D * STAGE);
   const unsigned char* tiles_p = s_raw + warp * (D * STAGE);
-  const T* X = (const T*)a.x;
-  const E* Z = kZ ? (const E*)a.z : (const E*)a.g;
+  const Source<T, T> X(a.x, C, c0, lane);
+  const Source<T, E> Z(kZ ? a.z : (const void*)a.g, C, c0, lane);
   auto request = [&](int j, int slot) {
     if (j < j1) {
-      fetch<T, T>(tiles + slot * STAGE, X, (int64_t)j * kSpan, b.end, C, c0, lane);
-      fetch<T, E>(tiles + slot * STAGE + XB, Z, (int64_t)j * kSpan, b.end, C, c0, lane);
+      X.fetch(tiles + slot * STAGE, j, b.end);
+      Z.fetch(tiles + slot * STAGE + XB, j, b.end);
     }
     copy_commit();
   };
@@ -387,13 +426,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
                             run.P.y < 0.f ? -1.f : run.P.y * A[i].y);
       }
     }
-#pragma unroll
-    for (int o = 1; o < GR; o <<= 1) {
-      const Map before = shuffle<true>(run, o * LC);
-      if (grp >= o) run = then(before, run);
-    }
-    Map before = shuffle<true>(run, LC);
-    if (grp == 0) before = Map{splat(1.f), splat(0.f)};
+    const Map before = cut ? compose<LC, true, false>(run, lane) : compose<LC, true, true>(run, lane);
 
     // the state (and, for a segment's map, the product) before this span
     float2 h_in = splat(0.f), p_in = splat(1.f);
@@ -423,12 +456,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 
     if (grp == 0) put2(a.states, j, C, c, in, h_in);
     float2 h = apply(before, h_in);
-    T* y = (T*)a.y + tk * C + c;
+    char* y = (char*)a.y + (tk * C + c) * (int64_t)sizeof(T);
+    const int pitch = C * (int)sizeof(T);
     if (!cut) {
 #pragma unroll
       for (int i = 0; i < K; ++i) {
         h = __ffma2_rn(A[i], h, B[i]);
-        if (in) stg2(y + (int64_t)i * C, h);
+        if (in) stg2((T*)(y + (int64_t)i * pitch), h);
       }
     } else {
       const uint32_t ends = (uint32_t)((marks.bits >> 1 | (uint64_t)marks.last << 63) >> (grp * K)) &
@@ -444,7 +478,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
           h = __ffma2_rn(A[i], h, B[i]);
         }
         if (live) {
-          stg2(y + (int64_t)i * C, h);
+          stg2((T*)(y + (int64_t)i * pitch), h);
           if (ends >> i & 1) put2(a.h_final, n, C, c, true, h);
         }
       }
@@ -464,7 +498,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   using G = Geo<T>;
   using E = typename std::conditional<kZ, T, float>::type;
   constexpr int XB = tile_bytes<T, T>(), ZB = tile_bytes<T, E>(), STAGE = 2 * XB + ZB, D = 2;
-  constexpr int K = G::K, LC = G::LC, GR = G::GR, CB = G::CB;
+  constexpr int K = G::K, LC = G::LC, CB = G::CB;
   extern __shared__ __align__(16) unsigned char s_raw[];
   __shared__ float2 s_h[LC], s_p[LC], s_dA[kMaxWarps][LC];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
@@ -496,13 +530,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   }
   const uint32_t tiles = (uint32_t)__cvta_generic_to_shared(s_raw) + warp * (D * STAGE);
   const unsigned char* tiles_p = s_raw + warp * (D * STAGE);
-  const E* Z = kZ ? (const E*)a.z : (const E*)a.g;
+  const Source<T, T> X(a.x, C, c0, lane), DY(a.dy, C, c0, lane);
+  const Source<T, E> Z(kZ ? a.z : (const void*)a.g, C, c0, lane);
   auto request = [&](int j, int slot) {
     if (j >= j0) {
-      const int64_t t0 = (int64_t)j * kSpan;
-      if (!kMaps) fetch<T, T>(tiles + slot * STAGE, a.x, t0, b.end, C, c0, lane);
-      fetch<T, T>(tiles + slot * STAGE + XB, a.dy, t0, b.end, C, c0, lane);
-      fetch<T, E>(tiles + slot * STAGE + 2 * XB, Z, t0, b.end, C, c0, lane);
+      if (!kMaps) X.fetch(tiles + slot * STAGE, j, b.end);
+      DY.fetch(tiles + slot * STAGE + XB, j, b.end);
+      Z.fetch(tiles + slot * STAGE + 2 * XB, j, b.end);
     }
     copy_commit();
   };
@@ -587,23 +621,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       }
       bwd.P = open ? P : splat(-1.f);
     }
-    Map before{splat(1.f), splat(0.f)};
-    if (!kMaps) {
-#pragma unroll
-      for (int o = 1; o < GR; o <<= 1) {
-        const Map m = shuffle<true>(fwd, o * LC);
-        if (grp >= o) fwd = then(m, fwd);
-      }
-      before = shuffle<true>(fwd, LC);
-      if (grp == 0) before = Map{splat(1.f), splat(0.f)};
+    Map before{splat(1.f), splat(0.f)}, after;
+    if (cut) {
+      if (!kMaps) before = compose<LC, true, false>(fwd, lane);
+      after = compose<LC, false, false>(bwd, lane);
+    } else {
+      if (!kMaps) before = compose<LC, true, true>(fwd, lane);
+      after = compose<LC, false, true>(bwd, lane);
     }
-#pragma unroll
-    for (int o = 1; o < GR; o <<= 1) {
-      const Map m = shuffle<false>(bwd, o * LC);
-      if (grp + o < GR) bwd = then(m, bwd);
-    }
-    Map after = shuffle<false>(bwd, LC);
-    if (grp == GR - 1) after = Map{splat(1.f), splat(0.f)};
 
     float2 l_in = splat(0.f), p_in = splat(1.f);
     if (j < j1 - 1) {
@@ -644,7 +669,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       h = __ffma2_rn(A[i], h, H[i]);
       H[i] = now;
     }
-    const int64_t at = tk * C + c;
+    const int pitch = C * (int)sizeof(T), pitch_g = C * 4;
+    char* dx = (char*)a.dx + (tk * C + c) * (int64_t)sizeof(T);
+    char* dg = kZ ? (char*)a.dz + (tk * C + c) * (int64_t)sizeof(T)
+                  : (char*)a.dg + (tk * C + c) * (int64_t)4;
 #pragma unroll
     for (int i = K - 1; i >= 0; --i) {
       const bool live = in && (!cut || tk + i < b.end);
@@ -657,16 +685,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       if (kZ) {
         const float2 z = lds2(sz + i * CB);
         const GateZ g = gate_z<true>(z, k);
-        const float2 d = __fadd2_rn(H[i], neg(lds2(sx + i * CB)));
+        const float2 d = __ffma2_rn(lds2(sx + i * CB), splat(-1.f), H[i]);
         const float2 dz = __fmul2_rn(__fmul2_rn(back, d), __fmul2_rn(g.p, kz));
         if (live) {
-          stg2((T*)a.dx + at + (int64_t)i * C, __fmul2_rn(g.m, lam));
-          stg2((T*)a.dz + at + (int64_t)i * C, dz);
+          stg2((T*)(dx + (int64_t)i * pitch), __fmul2_rn(g.m, lam));
+          stg2((T*)(dg + (int64_t)i * pitch), dz);
           dA_span = __ffma2_rn(dz, z, dA_span);
         }
       } else if (live) {
-        stg2((T*)a.dx + at + (int64_t)i * C, lam);
-        stg2(a.dg + at + (int64_t)i * C, __fmul2_rn(back, H[i]));
+        stg2((T*)(dx + (int64_t)i * pitch), lam);
+        stg2((float*)(dg + (int64_t)i * pitch_g), __fmul2_rn(back, H[i]));
       }
       if (cut && (starts >> i & 1)) {
         n = b.down(n, tk + i);
@@ -733,7 +761,7 @@ int segments(int T, int cols) {
 struct Plan {
   int cols, segs, seg_spans, warps, smem;
 };
-// Warps and shared memory: one block of up to 15 warps on an SM, or two of 8
+// Warps and shared memory: one block of up to 12 warps on an SM, or two of 6
 // when there are more blocks than SMs.
 Plan plan(const ScanArgs& a, int CB, int slot_bytes, bool one_segment) {
   Plan p;
@@ -744,7 +772,7 @@ Plan plan(const ScanArgs& a, int CB, int slot_bytes, bool one_segment) {
   if (p.seg_spans < 1) p.seg_spans = 1;
   p.segs = spans > 0 ? (spans + p.seg_spans - 1) / p.seg_spans : 1;
   const bool two = (int64_t)p.cols * p.segs > 148;
-  const int room = two ? kRoom / 2 - 1024 : kRoom, most = two ? 8 : kMaxWarps;
+  const int room = two ? kRoom / 2 - 1024 : kRoom, most = two ? kMaxWarps / 2 : kMaxWarps;
   p.warps = room / slot_bytes < most ? room / slot_bytes : most;
   if (p.warps > p.seg_spans) p.warps = p.seg_spans;
   p.smem = p.warps * slot_bytes;

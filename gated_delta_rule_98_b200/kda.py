@@ -648,8 +648,9 @@ def short_conv_swish(x, w, *, cu_seqlens=None, num_seqs=None, max_seqlen=None, y
 
 def _packed(x, cu_seqlens, num_seqs, max_seqlen):
     """(tokens, channels, sequences, longest) of a packed [T, ...] tensor."""
-    T = x.shape[0]
-    C = x.numel() // T if T else int(np.prod(x.shape[1:]))
+    shape = x.shape
+    T = shape[0]
+    C = shape[1] if len(shape) == 2 else int(np.prod(shape[1:]))
     if cu_seqlens is None:
         N = 1 if num_seqs is None else int(num_seqs)
         return T, C, N, T // N if N else 0
@@ -658,42 +659,50 @@ def _packed(x, cu_seqlens, num_seqs, max_seqlen):
     return T, C, cu_seqlens.numel() - 1, int(max_seqlen)
 
 
-def _roles(device, **ts):
-    """Raise ValueError unless every tensor given is on ``device``, contiguous and
-    of its role's (shape, dtype); ts: name = (tensor, shape, dtype)."""
-    for name, (t, shape, dtype) in ts.items():
-        if t is None:
-            continue
-        if t.device != device:
-            raise ValueError(f"{name}: on {t.device}, expected {device}")
-        if t.dtype != dtype or t.shape != shape:
-            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} "
-                             f"{dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
+def _role(name, t, shape, dtype, device):
+    """Raise ValueError unless t is on ``device``, contiguous, and of its role's
+    shape and dtype.  Returns its address (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected contiguous "
+                         f"{tuple(shape)} {dtype} on {device}")
+    return t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _call(fn, device, stream, *args):
-    """Run a C entry point on the tensors' device and raise unless it returns KDA_OK."""
+    """Run a C entry point on the tensors' device and its current stream (or
+    ``stream``), and raise unless it returns KDA_OK."""
     if device.type != "cuda":
         raise ValueError("KDA runs on the GPU only: pass CUDA tensors")
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            st = fn(*args, _stream(stream))
+    if stream is not None:
+        stream = stream.cuda_stream
+    elif _raw_stream is not None:
+        stream = _raw_stream(device.index)
     else:
-        st = fn(*args, _stream(stream))
+        stream = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, stream)
     if st != KDA_OK:
         raise KdaError(st, fn.__name__)
 
 
 def _workspace_of(nbytes, ws, device, what):
+    """(tensor, address, bytes) of a call's workspace; the caller keeps the tensor
+    until it has enqueued its work."""
     if nbytes == 0:
         raise KdaError(KDA_ERR_UNSUPPORTED, what)
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
         raise ValueError(f"workspace: contiguous uint8 on {device} expected")
-    return ws
+    return ws, ws.data_ptr(), ws.numel()
 
 
 def short_conv_swish_backward(x, w, dy, *, cu_seqlens=None, num_seqs=None, max_seqlen=None,
@@ -703,42 +712,44 @@ def short_conv_swish_backward(x, w, dy, *, cu_seqlens=None, num_seqs=None, max_s
     cu_seqlens[N] on (a padded batch) are left as they were in dx."""
     T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
     width = w.shape[-1]
-    dev, f32 = x.device, torch.float32
+    dev, dt, f32, shape, taps = x.device, x.dtype, torch.float32, x.shape, (C, width)
+    xp, wp = _role("x", x, shape, dt, dev), _role("w", w, taps, f32, dev)
+    dyp = _role("dy", dy, shape, dt, dev)
+    cup = _role("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
     if dx is None:
         dx = torch.empty_like(x)
     if dw is None:
-        dw = torch.empty((C, width), dtype=f32, device=dev)
-    _roles(dev, x=(x, x.shape, x.dtype), w=(w, (C, width), f32), dy=(dy, x.shape, x.dtype),
-           dx=(dx, x.shape, x.dtype), dw=(dw, (C, width), f32),
-           cu_seqlens=(cu_seqlens, (N + 1,), torch.int32))
-    ws = _workspace_of(kda_short_conv_swish_backward_workspace_size(T, C, width), workspace, dev,
-                       "kda_short_conv_swish_backward_workspace_size")
-    _call(kda_short_conv_swish_backward, dev, stream, _p(x), _p(w), _p(dy), _p(cu_seqlens), N, T,
-          L, C, width, _dt(x), _p(dx), _p(dw), _p(ws), ws.numel())
+        dw = torch.empty_like(w)
+    ws, wsp, nbytes = _workspace_of(
+        lib().kda_short_conv_swish_backward_workspace_size(T, C, width), workspace, dev,
+        "kda_short_conv_swish_backward_workspace_size")
+    _call(kda_short_conv_swish_backward, dev, stream, xp, wp, dyp, cup, N, T, L, C, width,
+          _dt(x), _role("dx", dx, shape, dt, dev), _role("dw", dw, taps, f32, dev), wsp, nbytes)
     return dx, dw
 
 
 def _gated_scan(x, z, A, g, h0, cu_seqlens, num_seqs, max_seqlen, y, h_final, states,
                 save_states, ws, stream):
     T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
-    dev, f32 = x.device, torch.float32
+    dev, dt, f32, shape, per_seq = x.device, x.dtype, torch.float32, x.shape, (N, C)
+    rows = ((T + KDA_SCAN_INTERVAL - 1) // KDA_SCAN_INTERVAL, C)
+    xp, h0p = _role("x", x, shape, dt, dev), _role("h0", h0, per_seq, f32, dev)
+    cup = _role("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
+    if z is None:
+        fn, gate = kda_gated_scan_g, (_role("g", g, shape, f32, dev),)
+    else:
+        fn, gate = kda_gated_scan, (_role("z", z, shape, dt, dev), _role("A", A, (C,), f32, dev))
     if y is None:
         y = torch.empty_like(x)
     if h_final is None:
-        h_final = torch.empty((N, C), dtype=f32, device=dev)
-    rows = (T + KDA_SCAN_INTERVAL - 1) // KDA_SCAN_INTERVAL
+        h_final = torch.empty(per_seq, dtype=f32, device=dev)
     if states is None and save_states:
-        states = torch.empty((rows, C), dtype=f32, device=dev)
-    _roles(dev, x=(x, x.shape, x.dtype), z=(z, x.shape, x.dtype), A=(A, (C,), f32),
-           g=(g, x.shape, f32), h0=(h0, (N, C), f32), y=(y, x.shape, x.dtype),
-           h_final=(h_final, (N, C), f32), states=(states, (rows, C), f32),
-           cu_seqlens=(cu_seqlens, (N + 1,), torch.int32))
-    ws = _workspace_of(kda_gated_scan_workspace_size(T, C), ws, dev,
-                       "kda_gated_scan_workspace_size")
-    gate = (_p(g),) if z is None else (_p(z), _p(A))
-    _call(kda_gated_scan_g if z is None else kda_gated_scan, dev, stream, _p(x), *gate, _p(h0),
-          _p(cu_seqlens), N, T, L, C, _dt(x), _p(y), _p(h_final), _p(states), _p(ws),
-          ws.numel())
+        states = torch.empty(rows, dtype=f32, device=dev)
+    ws, wsp, nbytes = _workspace_of(lib().kda_gated_scan_workspace_size(T, C), ws, dev,
+                                    "kda_gated_scan_workspace_size")
+    _call(fn, dev, stream, xp, *gate, h0p, cup, N, T, L, C, _dt(x),
+          _role("y", y, shape, dt, dev), _role("h_final", h_final, per_seq, f32, dev),
+          _role("states", states, rows, f32, dev), wsp, nbytes)
     return (y, h_final) if states is None else (y, h_final, states)
 
 
@@ -768,25 +779,27 @@ def gated_scan_g(x, g, *, h0=None, cu_seqlens=None, num_seqs=None, max_seqlen=No
 def _gated_scan_backward(x, z, A, g, states, dy, h0, dh_final, cu_seqlens, num_seqs, max_seqlen,
                          ws, stream):
     T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
-    dev, f32 = x.device, torch.float32
-    rows = (T + KDA_SCAN_INTERVAL - 1) // KDA_SCAN_INTERVAL
-    _roles(dev, x=(x, x.shape, x.dtype), z=(z, x.shape, x.dtype), A=(A, (C,), f32),
-           g=(g, x.shape, f32), states=(states, (rows, C), f32), dy=(dy, x.shape, x.dtype),
-           h0=(h0, (N, C), f32), dh_final=(dh_final, (N, C), f32),
-           cu_seqlens=(cu_seqlens, (N + 1,), torch.int32))
-    dx, dh0 = torch.empty_like(x), torch.empty((N, C), dtype=f32, device=dev)
-    ws = _workspace_of(kda_gated_scan_workspace_size(T, C), ws, dev,
-                       "kda_gated_scan_workspace_size")
+    dev, dt, f32, shape, per_seq = x.device, x.dtype, torch.float32, x.shape, (N, C)
+    rows = ((T + KDA_SCAN_INTERVAL - 1) // KDA_SCAN_INTERVAL, C)
+    xp = _role("x", x, shape, dt, dev)
+    common = (_role("states", states, rows, f32, dev), _role("h0", h0, per_seq, f32, dev),
+              _role("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev), N, T, L, C, _dt(x),
+              _role("dy", dy, shape, dt, dev), _role("dh_final", dh_final, per_seq, f32, dev))
+    if z is None:
+        gp = _role("g", g, shape, f32, dev)
+    else:
+        zp, Ap = _role("z", z, shape, dt, dev), _role("A", A, (C,), f32, dev)
+    dx, dh0 = torch.empty_like(x), torch.empty(per_seq, dtype=f32, device=dev)
+    ws, wsp, nbytes = _workspace_of(lib().kda_gated_scan_workspace_size(T, C), ws, dev,
+                                    "kda_gated_scan_workspace_size")
     if z is None:
         dg = torch.empty_like(g)
-        _call(kda_gated_scan_g_backward, dev, stream, _p(x), _p(g), _p(states), _p(h0),
-              _p(cu_seqlens), N, T, L, C, _dt(x), _p(dy), _p(dh_final), _p(dx), _p(dg), _p(dh0),
-              _p(ws), ws.numel())
+        _call(kda_gated_scan_g_backward, dev, stream, xp, gp, *common, dx.data_ptr(),
+              dg.data_ptr(), dh0.data_ptr(), wsp, nbytes)
         return dx, dg, dh0
     dz, dA = torch.empty_like(z), torch.empty_like(A)
-    _call(kda_gated_scan_backward, dev, stream, _p(x), _p(z), _p(A), _p(states), _p(h0),
-          _p(cu_seqlens), N, T, L, C, _dt(x), _p(dy), _p(dh_final), _p(dx), _p(dz), _p(dA),
-          _p(dh0), _p(ws), ws.numel())
+    _call(kda_gated_scan_backward, dev, stream, xp, zp, Ap, *common, dx.data_ptr(),
+          dz.data_ptr(), dA.data_ptr(), dh0.data_ptr(), wsp, nbytes)
     return dx, dz, dA, dh0
 
 
@@ -810,36 +823,39 @@ def gated_scan_step(x, z, A, h, *, y=None, stream=None):
     """One step of gated_scan for B sequences: x, z [B, ...], A [channels] fp32;
     h [B, channels] fp32 is updated in place.  Returns y (x's shape and dtype)."""
     B, C, _, _ = _packed(x, None, 1, None)
+    dev, dt, f32, shape = x.device, x.dtype, torch.float32, x.shape
     if y is None:
         y = torch.empty_like(x)
-    f32 = torch.float32
-    _roles(x.device, x=(x, x.shape, x.dtype), z=(z, x.shape, x.dtype), A=(A, (C,), f32),
-           h=(h, (B, C), f32), y=(y, x.shape, x.dtype))
-    _call(kda_gated_scan_step, x.device, stream, _p(x), _p(z), _p(A), _p(h), B, C, _dt(x), _p(y))
+    _call(kda_gated_scan_step, dev, stream, _role("x", x, shape, dt, dev),
+          _role("z", z, shape, dt, dev), _role("A", A, (C,), f32, dev),
+          _role("h", h, (B, C), f32, dev), B, C, _dt(x), _role("y", y, shape, dt, dev))
     return y
 
 
-def _head_rows(name, t, like, dtype, device):
-    """Token stride of a [T, heads, d] tensor whose heads lie side by side."""
-    if t.device != device or t.dtype != dtype or t.shape != like.shape or t.dim() != 3:
+def _head_rows(name, t, shape, dtype, device):
+    """(address, token stride) of a [T, heads, d] tensor whose heads lie side by side."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected "
-                         f"{tuple(like.shape)} {dtype} on {device}")
-    T, H, d = t.shape
-    if t.numel() and ((d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d)):
+                         f"{tuple(shape)} {dtype} on {device}")
+    T, H, d = shape
+    st, sh, sd = t.stride()
+    if t.numel() and (sd != 1 or (H > 1 and sh != d)):
         raise ValueError(f"{name}: heads must lie side by side (strides {t.stride()})")
-    return t.stride(0) if T > 1 else H * d
+    return t.data_ptr(), (st if T > 1 else H * d)
 
 
 def _qk(q, k, positions, freqs, q_weight, k_weight):
+    """(T, d, rot) and the addresses of what both directions read besides q and k."""
     dev, f32 = q.device, torch.float32
     if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
         raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}: [T, Hq, d] and [T, Hk, d] "
                          "expected")
     T, _, d = q.shape
-    _roles(dev, positions=(positions, (T,), torch.int32),
-           freqs=(freqs, (freqs.numel(),), torch.float64), q_weight=(q_weight, (d,), f32),
-           k_weight=(k_weight, (d,), f32))
-    return T, d, 2 * freqs.numel()
+    half = freqs.numel()
+    return T, d, 2 * half, (_role("positions", positions, (T,), torch.int32, dev),
+                            _role("freqs", freqs, (half,), torch.float64, dev),
+                            _role("q_weight", q_weight, (d,), f32, dev),
+                            _role("k_weight", k_weight, (d,), f32, dev))
 
 
 def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e-6,
@@ -850,17 +866,16 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     channels, paired (i, i + rot/2), or (2i, 2i+1) when ``interleaved``.  q and
     k may be slices of one projection's output (heads side by side, any token
     stride); q_out = q, k_out = k works in place.  Returns (q_out, k_out)."""
-    T, d, rot = _qk(q, k, positions, freqs, q_weight, k_weight)
-    dev, dt = q.device, q.dtype
+    T, d, rot, read = _qk(q, k, positions, freqs, q_weight, k_weight)
+    dev, dt, qs, ks = q.device, q.dtype, q.shape, k.shape
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=dev)
+        q_out = torch.empty(qs, dtype=dt, device=dev)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=dt, device=dev)
-    qs, ks = _head_rows("q", q, q, dt, dev), _head_rows("k", k, k, dt, dev)
-    qos, kos = _head_rows("q_out", q_out, q, dt, dev), _head_rows("k_out", k_out, k, dt, dev)
-    _call(kda_qk_norm_rope, dev, stream, _p(q), qs, _p(k), ks, _p(positions), _p(freqs),
-          _p(q_weight), _p(k_weight), float(eps), T, q.shape[1], k.shape[1], d, rot,
-          int(interleaved), _dt(q), _p(q_out), qos, _p(k_out), kos)
+        k_out = torch.empty(ks, dtype=dt, device=dev)
+    _call(kda_qk_norm_rope, dev, stream, *_head_rows("q", q, qs, dt, dev),
+          *_head_rows("k", k, ks, dt, dev), *read, eps, T, qs[1], ks[1], d, rot,
+          1 if interleaved else 0, _dt(q), *_head_rows("q_out", q_out, qs, dt, dev),
+          *_head_rows("k_out", k_out, ks, dt, dev))
     return q_out, k_out
 
 
@@ -871,23 +886,22 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, positions, freqs, *, q_weight=No
     rest as given to it; dq = dq_out, dk = dk_out works in place.  Returns
     (dq, dk, dq_weight, dk_weight), the last two [d] fp32 or None where the
     gain is None."""
-    T, d, rot = _qk(q, k, positions, freqs, q_weight, k_weight)
-    dev, dt = q.device, q.dtype
+    T, d, rot, read = _qk(q, k, positions, freqs, q_weight, k_weight)
+    dev, dt, qs, ks = q.device, q.dtype, q.shape, k.shape
     if dq is None:
-        dq = torch.empty(q.shape, dtype=dt, device=dev)
+        dq = torch.empty(qs, dtype=dt, device=dev)
     if dk is None:
-        dk = torch.empty(k.shape, dtype=dt, device=dev)
-    s = [_head_rows(name, t, like, dt, dev) for name, t, like in
-         (("q", q, q), ("k", k, k), ("dq_out", dq_out, q), ("dk_out", dk_out, k), ("dq", dq, q),
-          ("dk", dk, k))]
+        dk = torch.empty(ks, dtype=dt, device=dev)
     dqw = None if q_weight is None else torch.empty_like(q_weight)
     dkw = None if k_weight is None else torch.empty_like(k_weight)
-    ws = _workspace_of(kda_qk_norm_rope_backward_workspace_size(T, d), workspace, dev,
-                       "kda_qk_norm_rope_backward_workspace_size")
-    _call(kda_qk_norm_rope_backward, dev, stream, _p(q), s[0], _p(k), s[1], _p(dq_out), s[2],
-          _p(dk_out), s[3], _p(positions), _p(freqs), _p(q_weight), _p(k_weight), float(eps), T,
-          q.shape[1], k.shape[1], d, rot, int(interleaved), _dt(q), _p(dq), s[4], _p(dk), s[5],
-          _p(dqw), _p(dkw), _p(ws), ws.numel())
+    ws, wsp, nbytes = _workspace_of(lib().kda_qk_norm_rope_backward_workspace_size(T, d),
+                                    workspace, dev, "kda_qk_norm_rope_backward_workspace_size")
+    _call(kda_qk_norm_rope_backward, dev, stream, *_head_rows("q", q, qs, dt, dev),
+          *_head_rows("k", k, ks, dt, dev), *_head_rows("dq_out", dq_out, qs, dt, dev),
+          *_head_rows("dk_out", dk_out, ks, dt, dev), *read, eps, T, qs[1], ks[1], d, rot,
+          1 if interleaved else 0, _dt(q), *_head_rows("dq", dq, qs, dt, dev),
+          *_head_rows("dk", dk, ks, dt, dev), None if dqw is None else dqw.data_ptr(),
+          None if dkw is None else dkw.data_ptr(), wsp, nbytes)
     return dq, dk, dqw, dkw
 
 
