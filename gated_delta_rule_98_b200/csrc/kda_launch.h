@@ -102,7 +102,7 @@ struct ScanArgs {
   bool bf16;
   void* y;         // [T, C]
   float* h_final;  // [N, C] or null
-  float* states;   // [ceil(T / 64), C]: written by the forward (or null), read by the backward
+  float* states;   // [ceil(T / KDA_SCAN_INTERVAL), C]: written by the forward (or null), read by the backward
   void* ws;
   cudaStream_t stream;
   const void* dy = nullptr;  // [T, C]

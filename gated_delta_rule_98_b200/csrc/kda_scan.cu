@@ -11,10 +11,11 @@
 // tokens maps the state entering it to P h + H (P = prod a, H the run from 0),
 // and such maps compose, so tokens are worked on in parallel and only the
 // composition is sequential.  Three levels:
-//  * a thread owns 2 channels of 16 tokens (bf16; fp32: of 8) and runs them
-//    twice, once for (P, H) and once, from the state that enters, for h;
-//  * a warp owns a span of 64 tokens x 16 channels (32 bytes of a bf16 row;
-//    fp32: 8 channels) and composes its 4 (8) runs by shuffles;
+//  * a thread owns 2 channels of 8 tokens and runs them twice, once for (P, H)
+//    and once, from the state that enters, for h (longer runs compose less often
+//    but spill: 16 tokens took 128 registers' worth of decays alone);
+//  * a warp owns a span of 32 tokens x 16 channels of bf16 (64 x 8 of fp32: 32
+//    bytes of a row) and composes its 4 (8) runs by shuffles;
 //  * a block owns those channels of the whole token axis (or one of `segments`
 //    parts of it) and its warps take the spans in turn, handing the state from
 //    warp to warp through shared memory and a named barrier per warp.  A warp
@@ -34,6 +35,7 @@
 // as rounded y (2 bytes an element less to read, and no second rounding).
 #include <type_traits>
 
+#include "../../include/kda.h"
 #include "kda_common.cuh"
 #include "kda_launch.h"
 
@@ -41,8 +43,12 @@ namespace kda {
 
 namespace {
 
-constexpr int kSpan = 64;     // tokens of a span, and between saved states (KDA_SCAN_INTERVAL)
-constexpr int kMaxWarps = 12; // 168 registers a thread; at most 15 (a named barrier each)
+constexpr int kSaved = KDA_SCAN_INTERVAL;  // tokens between saved states
+// Warps of a block that has an SM to itself (half as many where two share one): at
+// most 15 (a named barrier each, 0 is __syncthreads), and what the registers allow.
+constexpr int kWarps = 15;      // forward: 128 registers a thread
+constexpr int kWarpsBack = 12;  // gradient: 168
+constexpr int kSlots = 3;     // spans of a warp in flight or in use
 constexpr int kMaxSegments = 64;
 constexpr int kRoom = 222 * 1024;  // dynamic shared memory of a block that has an SM to itself
 constexpr float kLog2e = 1.4426950408889634f;
@@ -71,27 +77,20 @@ __device__ __forceinline__ void stg2(__nv_bfloat16* p, float2 v) {
 }
 __device__ __forceinline__ void stg2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
 
-// a and 1 - a from t = g log2(e) in [-7.3, 0], both to a few units in the last
-// place: t = n + f, 2^f - 1 = f q(f) with q interpolated at the 6 Chebyshev nodes
-// of |f| <= 1/2 (2e-8 of it at most), a = 2^n + 2^n f q, 1 - a = (1 - 2^n) - 2^n f q.
-// Without the special function unit, which the sigmoid keeps busy.
+// a = 2^t and 1 - a, t = g log2(e) <= 0.  Near 1 the difference loses digits, so
+// above 2^-0.36 = 0.78 it is t times a polynomial: (1 - 2^t) / t interpolated at
+// the Chebyshev nodes of [-0.3605, 0] (a few units of 2^-24 there).
 __device__ __forceinline__ void decay(float2 t, float2& a, float2& m) {
-  const float2 magic = splat(12582912.f);  // 1.5 * 2^23: n lands in the low bits
-  const float2 r = __fadd2_rn(t, magic);
-  const float2 f = __fadd2_rn(t, __ffma2_rn(r, splat(-1.f), magic));
-  float2 q = splat(1.54531634e-4f);
-  q = __ffma2_rn(q, f, splat(1.33908633e-3f));
-  q = __ffma2_rn(q, f, splat(9.61808302e-3f));
-  q = __ffma2_rn(q, f, splat(5.55035695e-2f));
-  q = __ffma2_rn(q, f, splat(2.40226507e-1f));
-  q = __ffma2_rn(q, f, splat(6.93147182e-1f));
-  const float2 p = __fmul2_rn(q, f);
-  const uint32_t x = __float_as_uint(r.x) << 23, y = __float_as_uint(r.y) << 23;
-  const float2 s = make_float2(__uint_as_float(x + 0x3f800000u), __uint_as_float(y + 0x3f800000u));
-  const float2 ns =
-      make_float2(__uint_as_float(x + 0xbf800000u), __uint_as_float(y + 0xbf800000u));
-  a = __ffma2_rn(s, p, s);
-  m = __ffma2_rn(ns, p, __fadd2_rn(ns, splat(1.f)));
+  a = make_float2(ex2(t.x), ex2(t.y));
+  float2 q = splat(-0.00120225688f);
+  q = __ffma2_rn(q, t, splat(-0.00957753696f));
+  q = __ffma2_rn(q, t, splat(-0.0554989241f));
+  q = __ffma2_rn(q, t, splat(-0.240226269f));
+  q = __ffma2_rn(q, t, splat(-0.693147182f));
+  q = __fmul2_rn(q, t);
+  m = __ffma2_rn(a, splat(-1.f), splat(1.f));
+  m.x = t.x > -0.36f ? q.x : m.x;
+  m.y = t.y > -0.36f ? q.y : m.y;
 }
 
 // The library's gate on two channels: k = -e^A log2(e).
@@ -163,19 +162,19 @@ __device__ __forceinline__ Map compose(Map& run, int lane) {
   return at < LC ? Map{splat(1.f), splat(0.f)} : before;
 }
 
-// Tile geometry: rows of 32 bytes of x, 2 channels a lane.
-template <typename T>
+// Tile geometry: a span of SPAN tokens, rows of 32 bytes of x, 2 channels a lane.
+template <typename T, int SPAN>
 struct Geo {
   static constexpr int CB = 32 / (int)sizeof(T);  // channels of a block
   static constexpr int LC = CB / 2;               // lanes along the channels
   static constexpr int GR = 32 / LC;              // runs of a span
-  static constexpr int K = kSpan / GR;            // tokens of a run
+  static constexpr int K = SPAN / GR;             // tokens of a run
 };
 // Bytes of one tensor's span in shared memory: a spare row after each run moves
 // the runs to different banks, so that a warp's reads do not collide.
-template <typename T, typename E>
+template <typename G, typename E>
 __host__ __device__ constexpr int tile_bytes() {
-  return Geo<T>::GR * (Geo<T>::K + 1) * Geo<T>::CB * (int)sizeof(E);
+  return G::GR * (G::K + 1) * G::CB * (int)sizeof(E);
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
@@ -189,11 +188,11 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 // One tensor's way into a warp's slots: lane `lane` brings 16 bytes of a row, a
-// span takes kSpan * CH / 32 copies of 32 / CH rows each.
-template <typename T, typename E>
+// span takes COPIES copies of ROWS rows each.
+template <typename G, typename E>
 struct Source {
-  static constexpr int RB = Geo<T>::CB * (int)sizeof(E), CH = RB / 16, PER = 16 / (int)sizeof(E);
-  static constexpr int ROWS = 32 / CH, COPIES = kSpan / ROWS;
+  static constexpr int RB = G::CB * (int)sizeof(E), CH = RB / 16, PER = 16 / (int)sizeof(E);
+  static constexpr int SPAN = G::GR * G::K, ROWS = 32 / CH, COPIES = SPAN / ROWS;
   const char* base;
   const char* p;   // this lane's piece of the first copy's row of span 0
   int row, pitch;  // the row in that copy; bytes of a row of the tensor
@@ -206,17 +205,17 @@ struct Source {
     pitch = C * (int)sizeof(E);
     in = c0 + ch * PER < C;
     p = (const char*)src + (int64_t)row * pitch + (int64_t)(in ? c0 + ch * PER : 0) * sizeof(E);
-    dst = (row + row / Geo<T>::K) * RB + ch * 16;
+    dst = (row + row / G::K) * RB + ch * 16;
   }
   // Span j into the tile; zeros outside the tensor and from token `end` on.
   __device__ __forceinline__ void fetch(uint32_t tile, int j, int end) const {
-    const char* q = p + (int64_t)j * kSpan * pitch;
-    const int left = end - j * kSpan - row;  // rows from this lane's first one to the end
+    const char* q = p + (int64_t)j * SPAN * pitch;
+    const int left = end - j * SPAN - row;  // rows from this lane's first one to the end
 #pragma unroll
     for (int it = 0; it < COPIES; ++it) {
-      static_assert(ROWS % Geo<T>::K == 0 || Geo<T>::K % ROWS == 0, "spare rows");
+      static_assert(ROWS % G::K == 0 || G::K % ROWS == 0, "spare rows");
       const bool live = in && it * ROWS < left;
-      copy16(tile + dst + (it * ROWS + it * ROWS / Geo<T>::K) * RB,
+      copy16(tile + dst + (it * ROWS + it * ROWS / G::K) * RB,
              live ? q + (int64_t)(it * ROWS) * pitch : base, live);
     }
   }
@@ -264,40 +263,43 @@ struct Bounds {
   }
 };
 
-// Boundaries (sequence starts, and the end) at tokens [t0, t0 + 64]: bit i of
-// `bits` is token t0 + i, `last` is token t0 + 64.
+// Boundaries (sequence starts, and the end) at tokens [t0, t0 + SPAN]: bit i of
+// `bits` is token t0 + i, `last` is token t0 + SPAN.
 struct Marks {
   uint64_t bits;
   bool last;
   __device__ __forceinline__ bool any() const { return bits != 0 || last; }
 };
 // A warp's view of the boundaries of the spans it takes, in rising or falling
-// order: `clear` is how far from the last span no boundary lies.
-template <bool kRising>
+// order: no boundary lies between the last span and `clear`.
+template <bool kRising, int SPAN>
 struct Marker {
   int k = 0;
-  int64_t clear = kRising ? -1 : INT64_MAX;
-  __device__ __forceinline__ Marks look(const Bounds& b, int64_t t0, int lane) {
+  int clear = kRising ? -1 : 0x7fffffff;
+  __device__ __forceinline__ Marks look(const Bounds& b, int t0, int lane) {
     Marks m{0, false};
-    if (b.end == t0 + kSpan) m.last = true;
-    else if (b.end < t0 + kSpan) m.bits |= 1ull << (b.end - t0);
-    if (kRising ? clear > t0 + kSpan : clear < t0) return m;
+    const int t1 = t0 + SPAN;
+    const bool quiet = kRising ? clear > t1 : clear < t0;
+    if (quiet && b.end > t1) return m;
+    if (b.end == t1) m.last = true;
+    else if (b.end < t1) m.bits |= 1ull << (b.end - t0);
+    if (quiet) return m;
     k = b.lower(kRising ? min(k, b.N) : 0, t0);
-    if (kRising) clear = k <= b.N ? b.at(k) : INT64_MAX;      // first boundary from t0 on
-    else clear = k <= b.N && b.at(k) == t0 ? t0 : k > 0 ? b.at(k - 1) : -1;  // last one up to t0
-    uint32_t lo = 0, hi = 0, at64 = 0;
+    if (kRising) clear = k <= b.N ? (int)b.at(k) : 0x7fffffff;  // first boundary from t0 on
+    else clear = k <= b.N && b.at(k) == t0 ? t0 : k > 0 ? (int)b.at(k - 1) : -1;  // last up to t0
+    uint32_t lo = 0, hi = 0, at_end = 0;
     for (int i = k; i <= b.N; i += 32) {
       const int64_t v = i + lane <= b.N ? b.at(i + lane) - t0 : INT64_MAX;
-      if (v >= 0 && v < 32) lo |= 1u << v;
-      else if (v >= 32 && v < 64) hi |= 1u << (v - 32);
-      else if (v == 64) at64 = 1;
+      if (v == SPAN) at_end = 1;
+      else if (v >= 0 && v < 32) lo |= 1u << v;
+      else if (v >= 32 && v < SPAN) hi |= 1u << (v - 32);
       // entries do not fall, so a lane beyond the span ends the search
-      if (__any_sync(0xffffffffu, v > kSpan)) break;
+      if (__any_sync(0xffffffffu, v > SPAN)) break;
     }
     lo = __reduce_or_sync(0xffffffffu, lo);
     hi = __reduce_or_sync(0xffffffffu, hi);
     m.bits |= (uint64_t)hi << 32 | lo;
-    m.last |= __reduce_or_sync(0xffffffffu, at64) != 0;
+    m.last |= __reduce_or_sync(0xffffffffu, at_end) != 0;
     return m;
   }
 };
@@ -324,27 +326,27 @@ __device__ __forceinline__ void pass_empty(const Bounds& b, const float* from, f
 
 // kMaps: form the segment's map (P, H) in `maps` instead of y; else compose
 // the maps of the segments before this one.
-template <typename T, bool kZ, bool kMaps>
-__global__ void __launch_bounds__(kMaxWarps * 32, 1)
+template <typename T, bool kZ, bool kMaps, int SPAN>
+__global__ void __launch_bounds__(kWarps * 32, 1)
     scan_kernel(const ScanArgs a, int seg_spans, float* maps) {
-  using G = Geo<T>;
+  using G = Geo<T, SPAN>;
   using E = typename std::conditional<kZ, T, float>::type;
-  constexpr int XB = tile_bytes<T, T>(), STAGE = XB + tile_bytes<T, E>(), D = 3;
+  constexpr int XB = tile_bytes<G, T>(), STAGE = XB + tile_bytes<G, E>(), D = kSlots;
   constexpr int K = G::K, LC = G::LC, GR = G::GR, CB = G::CB;
   extern __shared__ __align__(16) unsigned char s_raw[];
-  __shared__ float2 s_h[LC], s_p[LC];
+  __shared__ float2 s_h[2][LC], s_p[2][LC];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
   const int l = lane % LC, grp = lane / LC;
   const int C = a.C, c0 = blockIdx.x * CB, c = c0 + 2 * l;
   const bool in = c < C;
   const Bounds b(a);
-  const int spans = (int)(((int64_t)b.end + kSpan - 1) / kSpan);
+  const int spans = (int)(((int64_t)b.end + SPAN - 1) / SPAN);
   int j0 = blockIdx.y * seg_spans;
   const int j1 = min(j0 + seg_spans, spans);
   if (kMaps) {
     // the map that later segments need: nothing before the last sequence start matters
     if (j0 >= j1 || j1 == spans) return;
-    const int64_t te = (int64_t)j1 * kSpan;
+    const int64_t te = (int64_t)j1 * SPAN;
     const int k = b.lower(0, te);
     if (k <= b.N && b.at(k) == te) {
       if (warp == 0 && grp == 0) {
@@ -353,15 +355,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       }
       return;
     }
-    if (k > 0) j0 = max(j0, (int)(max(b.at(k - 1), (int64_t)0) / kSpan));
+    if (k > 0) j0 = max(j0, (int)(max(b.at(k - 1), (int64_t)0) / SPAN));
   } else if (blockIdx.y == 0) {
     pass_empty(b, a.h0, a.h_final, C, c0, CB);
   }
   const uint32_t tiles =
       (uint32_t)__cvta_generic_to_shared(s_raw) + warp * (D * STAGE);
   const unsigned char* tiles_p = s_raw + warp * (D * STAGE);
-  const Source<T, T> X(a.x, C, c0, lane);
-  const Source<T, E> Z(kZ ? a.z : (const void*)a.g, C, c0, lane);
+  const Source<G, T> X(a.x, C, c0, lane);
+  const Source<G, E> Z(kZ ? a.z : (const void*)a.g, C, c0, lane);
   auto request = [&](int j, int slot) {
     if (j < j1) {
       X.fetch(tiles + slot * STAGE, j, b.end);
@@ -373,14 +375,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   for (int i = 0; i < D - 1; ++i) request(j0 + warp + i * W, i);
   float2 k = splat(0.f);
   if (kZ && in && b.end > 0) k = make_float2(-kLog2e * expf(a.A[c]), -kLog2e * expf(a.A[c + 1]));
-  Marker<true> marker;
+  Marker<true, SPAN> marker;
   int slot = 0;
   for (int j = j0 + warp; j < j1; j += W) {
     __syncwarp();
     request(j + (D - 1) * W, slot == 0 ? D - 1 : slot - 1);
     copy_wait<D - 1>();
     __syncwarp();
-    const int64_t t0 = (int64_t)j * kSpan, tk = t0 + grp * K;
+    const int t0 = j * SPAN, tk = t0 + grp * K;
     const T* sx = (const T*)(tiles_p + slot * STAGE) + grp * (K + 1) * CB + 2 * l;
     const E* sz = (const E*)(tiles_p + slot * STAGE + XB) + grp * (K + 1) * CB + 2 * l;
     slot = slot == D - 1 ? 0 : slot + 1;
@@ -401,14 +403,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         A[i] = make_float2(ex2(z.x * kLog2e), ex2(z.y * kLog2e));
         B[i] = x;
       }
+      // with no start inside; here, and not behind a branch, so that this chain
+      // runs between the gates' independent instructions
+      run.H = __ffma2_rn(A[i], run.H, B[i]);
+      run.P = __fmul2_rn(run.P, A[i]);
     }
-    if (!cut) {
-#pragma unroll
-      for (int i = 0; i < K; ++i) {
-        run.H = __ffma2_rn(A[i], run.H, B[i]);
-        run.P = __fmul2_rn(run.P, A[i]);
-      }
-    } else {
+    if (cut) {
+      run = Map{splat(1.f), splat(0.f)};
       int n = starts ? b.of(tk) : 0;
 #pragma unroll
       for (int i = 0; i < K; ++i) {
@@ -432,19 +433,19 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     float2 h_in = splat(0.f), p_in = splat(1.f);
     if (j > j0) {
       if (W > 1) turn_wait(warp);
-      h_in = s_h[l];
-      if (kMaps) p_in = s_p[l];
+      h_in = s_h[j & 1][l];
+      if (kMaps) p_in = s_p[j & 1][l];
     } else if (!kMaps) {
       for (int s = 0; s < (int)blockIdx.y; ++s)
         h_in = apply(Map{row2(maps, 2 * s, C, c, in), row2(maps, 2 * s + 1, C, c, in)}, h_in);
     }
-    __syncwarp();
+    // slot j + 1 was last read by the warp of span j - 1, before it passed the turn
     const float2 h_out = apply(run, h_in);
     float2 p_out = p_in;
     if (kMaps) p_out = make_float2(then_p(p_in.x, run.P.x), then_p(p_in.y, run.P.y));
     if (grp == GR - 1) {
-      s_h[l] = h_out;
-      if (kMaps) s_p[l] = p_out;
+      s_h[(j + 1) & 1][l] = h_out;
+      if (kMaps) s_p[(j + 1) & 1][l] = p_out;
       if (kMaps && j == j1 - 1) {
         put2(maps, 2 * blockIdx.y, C, c, in, p_out);
         put2(maps, 2 * blockIdx.y + 1, C, c, in, h_out);
@@ -454,9 +455,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     if (j + 1 < j1 && W > 1) turn_pass(warp + 1 == W ? 0 : warp + 1);
     if (kMaps) continue;
 
-    if (grp == 0) put2(a.states, j, C, c, in, h_in);
     float2 h = apply(before, h_in);
-    char* y = (char*)a.y + (tk * C + c) * (int64_t)sizeof(T);
+    if (grp * K % kSaved == 0 && tk < b.end) put2(a.states, tk / kSaved, C, c, in, h);
+    char* y = (char*)a.y + ((int64_t)tk * C + c) * (int64_t)sizeof(T);
     const int pitch = C * (int)sizeof(T);
     if (!cut) {
 #pragma unroll
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         if (in) stg2((T*)(y + (int64_t)i * pitch), h);
       }
     } else {
-      const uint32_t ends = (uint32_t)((marks.bits >> 1 | (uint64_t)marks.last << 63) >> (grp * K)) &
+      const uint32_t ends = (uint32_t)((marks.bits >> 1 | (uint64_t)marks.last << (SPAN - 1)) >> (grp * K)) &
                             ((1u << K) - 1);
       int n = (starts | ends) ? b.of(tk) : 0;
 #pragma unroll
@@ -492,27 +493,27 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 // kMaps: form the map of the gradient through the segment, from its last token
 // to its first, in `maps`; else compose the maps of the segments after this
 // one.  dA of the segment's tokens goes to row blockIdx.y of dA_part.
-template <typename T, bool kZ, bool kMaps>
-__global__ void __launch_bounds__(kMaxWarps * 32, 1)
+template <typename T, bool kZ, bool kMaps, int SPAN>
+__global__ void __launch_bounds__(kWarpsBack * 32, 1)
     scan_backward_kernel(const ScanArgs a, int seg_spans, float* maps, float* dA_part) {
-  using G = Geo<T>;
+  using G = Geo<T, SPAN>;
   using E = typename std::conditional<kZ, T, float>::type;
-  constexpr int XB = tile_bytes<T, T>(), ZB = tile_bytes<T, E>(), STAGE = 2 * XB + ZB, D = 2;
+  constexpr int XB = tile_bytes<G, T>(), ZB = tile_bytes<G, E>(), STAGE = 2 * XB + ZB, D = kSlots;
   constexpr int K = G::K, LC = G::LC, CB = G::CB;
   extern __shared__ __align__(16) unsigned char s_raw[];
-  __shared__ float2 s_h[LC], s_p[LC], s_dA[kMaxWarps][LC];
+  __shared__ float2 s_h[2][LC], s_p[2][LC], s_dA[kWarpsBack][LC];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
   const int l = lane % LC, grp = lane / LC;
   const int C = a.C, c0 = blockIdx.x * CB, c = c0 + 2 * l;
   const bool in = c < C;
   const Bounds b(a);
-  const int spans = (int)(((int64_t)b.end + kSpan - 1) / kSpan);
+  const int spans = (int)(((int64_t)b.end + SPAN - 1) / SPAN);
   const int j0 = blockIdx.y * seg_spans;
   int j1 = min(j0 + seg_spans, spans);
   if (kMaps) {
     // the map that earlier segments need: nothing after the first sequence end matters
     if (j0 >= j1 || j0 == 0) return;
-    const int64_t ts = (int64_t)j0 * kSpan;
+    const int64_t ts = (int64_t)j0 * SPAN;
     const int k = b.lower(0, ts);
     if (k <= b.N && b.at(k) == ts) {
       if (warp == 0 && grp == 0) {
@@ -523,15 +524,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     }
     if (k <= b.N) {
       const int64_t e = min(b.at(k), (int64_t)b.end);
-      j1 = min(j1, (int)((e + kSpan - 1) / kSpan));
+      j1 = min(j1, (int)((e + SPAN - 1) / SPAN));
     }
   } else if (blockIdx.y == 0) {
     pass_empty(b, a.dh_final, a.dh0, C, c0, CB);
   }
   const uint32_t tiles = (uint32_t)__cvta_generic_to_shared(s_raw) + warp * (D * STAGE);
   const unsigned char* tiles_p = s_raw + warp * (D * STAGE);
-  const Source<T, T> X(a.x, C, c0, lane), DY(a.dy, C, c0, lane);
-  const Source<T, E> Z(kZ ? a.z : (const void*)a.g, C, c0, lane);
+  const Source<G, T> X(a.x, C, c0, lane), DY(a.dy, C, c0, lane);
+  const Source<G, E> Z(kZ ? a.z : (const void*)a.g, C, c0, lane);
   auto request = [&](int j, int slot) {
     if (j >= j0) {
       if (!kMaps) X.fetch(tiles + slot * STAGE, j, b.end);
@@ -547,15 +548,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   // -5 e^A, the constant factors of dz
   const float2 kz = __fmul2_rn(k, splat(-kGateMin / kLog2e));
   float2 dA = splat(0.f);
-  Marker<false> marker;
+  Marker<false, SPAN> marker;
   int slot = 0;
   for (int j = j1 - 1 - warp; j >= j0; j -= W) {
     __syncwarp();
     request(j - (D - 1) * W, slot == 0 ? D - 1 : slot - 1);
-    const float2 state = kMaps ? splat(0.f) : row2(a.states, j, C, c, in);
+    const float2 state = kMaps ? splat(0.f) : row2(a.states, j * (SPAN / kSaved), C, c, in);
     copy_wait<D - 1>();
     __syncwarp();
-    const int64_t t0 = (int64_t)j * kSpan, tk = t0 + grp * K;
+    const int t0 = j * SPAN, tk = t0 + grp * K;
     const unsigned char* tile = tiles_p + slot * STAGE;
     const int off = grp * (K + 1) * CB + 2 * l;
     const T* sx = (const T*)tile + off;
@@ -566,34 +567,37 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     const bool cut = marks.any();
     const uint32_t starts = (uint32_t)(marks.bits >> (grp * K)) & ((1u << K) - 1);
     const uint32_t ends =
-        (uint32_t)((marks.bits >> 1 | (uint64_t)marks.last << 63) >> (grp * K)) & ((1u << K) - 1);
+        (uint32_t)((marks.bits >> 1 | (uint64_t)marks.last << (SPAN - 1)) >> (grp * K)) & ((1u << K) - 1);
 
     // fwd: the state through the run; bwd: the gradient that leaves its first token,
-    // for the gradient entering behind its last one
-    float2 A[K], H[K];
+    // for the gradient entering behind its last one.  The gate's decay, input scale
+    // and slope stay in registers for the second walk (8 tokens a run leave room)
+    float2 A[K], H[K], M[kZ ? K : 1], S[kZ ? K : 1];
     Map fwd{splat(1.f), splat(0.f)}, bwd{splat(1.f), splat(0.f)};
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const float2 z = lds2(sz + i * CB);
       if (kZ) {
-        const GateZ g = gate_z<false>(z, k);
+        const GateZ g = gate_z<!kMaps>(z, k);
         A[i] = g.a;
-        if (!kMaps) H[i] = __fmul2_rn(g.m, lds2(sx + i * CB));
+        if (!kMaps) {
+          M[i] = g.m;
+          S[i] = g.p;
+          H[i] = __fmul2_rn(g.m, lds2(sx + i * CB));
+        }
       } else {
         A[i] = make_float2(ex2(z.x * kLog2e), ex2(z.y * kLog2e));
         if (!kMaps) H[i] = lds2(sx + i * CB);
       }
+      // with no start inside, as in the forward
+      if (!kMaps) fwd.H = __ffma2_rn(A[i], fwd.H, H[i]);
+      bwd.P = __fmul2_rn(bwd.P, A[i]);
+      bwd.H = __ffma2_rn(bwd.P, lds2(sd + i * CB), bwd.H);
     }
+    fwd.P = bwd.P;
     int n_first = 0;
-    if (!cut) {
-#pragma unroll
-      for (int i = 0; i < K; ++i) {
-        if (!kMaps) fwd.H = __ffma2_rn(A[i], fwd.H, H[i]);
-        bwd.P = __fmul2_rn(bwd.P, A[i]);
-        bwd.H = __ffma2_rn(bwd.P, lds2(sd + i * CB), bwd.H);
-      }
-      fwd.P = bwd.P;
-    } else {
+    if (cut) {
+      fwd = bwd = Map{splat(1.f), splat(0.f)};
       n_first = (starts | ends) ? b.of(tk) : 0;
       int n = n_first;
       float2 P = splat(1.f);  // product up to the run's first sequence end
@@ -633,20 +637,19 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     float2 l_in = splat(0.f), p_in = splat(1.f);
     if (j < j1 - 1) {
       if (W > 1) turn_wait(warp);
-      l_in = s_h[l];
-      if (kMaps) p_in = s_p[l];
+      l_in = s_h[j & 1][l];
+      if (kMaps) p_in = s_p[j & 1][l];
     } else if (!kMaps) {
       const int last = (spans + seg_spans - 1) / seg_spans - 1;
       for (int s = last; s > (int)blockIdx.y; --s)
         l_in = apply(Map{row2(maps, 2 * s, C, c, in), row2(maps, 2 * s + 1, C, c, in)}, l_in);
     }
-    __syncwarp();
     const float2 l_out = apply(bwd, l_in);
     float2 p_out = p_in;
     if (kMaps) p_out = make_float2(then_p(p_in.x, bwd.P.x), then_p(p_in.y, bwd.P.y));
     if (grp == 0) {
-      s_h[l] = l_out;
-      if (kMaps) s_p[l] = p_out;
+      s_h[(j - 1) & 1][l] = l_out;
+      if (kMaps) s_p[(j - 1) & 1][l] = p_out;
       if (kMaps && j == j0) {
         put2(maps, 2 * blockIdx.y, C, c, in, p_out);
         put2(maps, 2 * blockIdx.y + 1, C, c, in, l_out);
@@ -658,47 +661,58 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 
     // the state before each token, in place of the token's input
     float2 h = apply(before, state), back = apply(after, l_in), dA_span = splat(0.f);
-    int n = n_first;
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-      if (cut && (starts >> i & 1)) {
-        n = b.up(n, tk + i);
-        h = row2(a.h0, n, C, c, in && tk + i < b.end);
-      }
-      const float2 now = h;
-      h = __ffma2_rn(A[i], h, H[i]);
-      H[i] = now;
-    }
-    const int pitch = C * (int)sizeof(T), pitch_g = C * 4;
-    char* dx = (char*)a.dx + (tk * C + c) * (int64_t)sizeof(T);
-    char* dg = kZ ? (char*)a.dz + (tk * C + c) * (int64_t)sizeof(T)
-                  : (char*)a.dg + (tk * C + c) * (int64_t)4;
-#pragma unroll
-    for (int i = K - 1; i >= 0; --i) {
-      const bool live = in && (!cut || tk + i < b.end);
-      if (cut && (ends >> i & 1)) {
-        n = b.down(n, tk + i);
-        back = row2(a.dh_final, n, C, c, live);
-      }
+    const int pitch = C * (int)sizeof(T), pitch_g = C * (int)sizeof(E);
+    char* dx = (char*)a.dx + ((int64_t)tk * C + c) * (int64_t)sizeof(T);
+    char* dg = (char*)(kZ ? a.dz : (void*)a.dg) + ((int64_t)tk * C + c) * (int64_t)sizeof(E);
+    auto token = [&](int i, bool live) {
       const float2 lam = __fadd2_rn(lds2(sd + i * CB), back);
       back = __fmul2_rn(A[i], lam);
       if (kZ) {
-        const float2 z = lds2(sz + i * CB);
-        const GateZ g = gate_z<true>(z, k);
         const float2 d = __ffma2_rn(lds2(sx + i * CB), splat(-1.f), H[i]);
-        const float2 dz = __fmul2_rn(__fmul2_rn(back, d), __fmul2_rn(g.p, kz));
+        const float2 dz = __fmul2_rn(__fmul2_rn(back, d), __fmul2_rn(S[i], kz));
         if (live) {
-          stg2((T*)(dx + (int64_t)i * pitch), __fmul2_rn(g.m, lam));
-          stg2((T*)(dg + (int64_t)i * pitch), dz);
-          dA_span = __ffma2_rn(dz, z, dA_span);
+          stg2((T*)(dx + (int64_t)i * pitch), __fmul2_rn(M[i], lam));
+          stg2((E*)(dg + (int64_t)i * pitch_g), dz);
+          dA_span = __ffma2_rn(dz, lds2(sz + i * CB), dA_span);
         }
       } else if (live) {
         stg2((T*)(dx + (int64_t)i * pitch), lam);
-        stg2((float*)(dg + (int64_t)i * pitch_g), __fmul2_rn(back, H[i]));
+        stg2((E*)(dg + (int64_t)i * pitch_g), __fmul2_rn(back, H[i]));
       }
-      if (cut && (starts >> i & 1)) {
-        n = b.down(n, tk + i);
-        put2(a.dh0, n, C, c, live, back);
+    };
+    if (!cut) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        const float2 now = h;
+        h = __ffma2_rn(A[i], h, H[i]);
+        H[i] = now;
+      }
+#pragma unroll
+      for (int i = K - 1; i >= 0; --i) token(i, in);
+    } else {
+      int n = n_first;
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        if (starts >> i & 1) {
+          n = b.up(n, tk + i);
+          h = row2(a.h0, n, C, c, in && tk + i < b.end);
+        }
+        const float2 now = h;
+        h = __ffma2_rn(A[i], h, H[i]);
+        H[i] = now;
+      }
+#pragma unroll
+      for (int i = K - 1; i >= 0; --i) {
+        const bool live = in && tk + i < b.end;
+        if (ends >> i & 1) {
+          n = b.down(n, tk + i);
+          back = row2(a.dh_final, n, C, c, live);
+        }
+        token(i, live);
+        if (starts >> i & 1) {
+          n = b.down(n, tk + i);
+          put2(a.dh0, n, C, c, live, back);
+        }
       }
     }
     dA = __fadd2_rn(dA, dA_span);
@@ -748,34 +762,33 @@ __global__ void __launch_bounds__(256)
 
 // ----------------------------------------------------------------- launch ----
 
-// Segments of the token axis: one block per SM and channel group at least,
-// segments of 16 spans at least.
+// Segments of the token axis: two blocks per SM at least when the channels
+// alone give few, segments of 1024 tokens at least.
 int segments(int T, int cols) {
-  const int spans = (int)(((int64_t)T + kSpan - 1) / kSpan);
   if (cols >= 100) return 1;
-  int s = 296 / cols;
-  s = s < spans / 16 ? s : spans / 16;
+  const int s = 296 / cols < T / 1024 ? 296 / cols : T / 1024;
   return s < 1 ? 1 : s > kMaxSegments ? kMaxSegments : s;
 }
 
 struct Plan {
   int cols, segs, seg_spans, warps, smem;
 };
-// Warps and shared memory: one block of up to 12 warps on an SM, or two of 6
-// when there are more blocks than SMs.
-Plan plan(const ScanArgs& a, int CB, int slot_bytes, bool one_segment) {
+// Warps and shared memory: one block of up to most_warps warps on an SM, or two
+// of half as many when there are more blocks than SMs.
+template <typename G>
+Plan plan(const ScanArgs& a, int warp_bytes, int most_warps, bool one_segment) {
+  constexpr int SPAN = G::GR * G::K;
   Plan p;
-  p.cols = (a.C + CB - 1) / CB;
-  p.segs = one_segment ? 1 : segments(a.T, p.cols);
-  const int spans = (int)(((int64_t)a.T + kSpan - 1) / kSpan);
-  p.seg_spans = (spans + p.segs - 1) / p.segs;
-  if (p.seg_spans < 1) p.seg_spans = 1;
+  p.cols = (a.C + G::CB - 1) / G::CB;
+  const int spans = (int)(((int64_t)a.T + SPAN - 1) / SPAN);
+  const int segs = one_segment ? 1 : segments(a.T, p.cols);
+  p.seg_spans = spans > 0 ? (spans + segs - 1) / segs : 1;
   p.segs = spans > 0 ? (spans + p.seg_spans - 1) / p.seg_spans : 1;
   const bool two = (int64_t)p.cols * p.segs > 148;
-  const int room = two ? kRoom / 2 - 1024 : kRoom, most = two ? kMaxWarps / 2 : kMaxWarps;
-  p.warps = room / slot_bytes < most ? room / slot_bytes : most;
+  const int room = two ? kRoom / 2 - 1024 : kRoom, most = two ? (most_warps + 1) / 2 : most_warps;
+  p.warps = room / warp_bytes < most ? room / warp_bytes : most;
   if (p.warps > p.seg_spans) p.warps = p.seg_spans;
-  p.smem = p.warps * slot_bytes;
+  p.smem = p.warps * warp_bytes;
   return p;
 }
 
@@ -787,41 +800,47 @@ cudaError_t allow(F* kernel) {
 
 template <typename T, bool kZ>
 cudaError_t forward_t(const ScanArgs& a) {
+  constexpr int SPAN = sizeof(T) == 2 ? 32 : 64;  // 8 tokens a run
+  using G = Geo<T, SPAN>;
   using E = typename std::conditional<kZ, T, float>::type;
-  const int slot = 3 * (tile_bytes<T, T>() + tile_bytes<T, E>());
   // a later segment writes h_final while an earlier one reads h0: not in place
-  const Plan p = plan(a, Geo<T>::CB, slot, a.h0 && a.h0 == a.h_final);
+  const Plan p = plan<G>(a, kSlots * (tile_bytes<G, T>() + tile_bytes<G, E>()), kWarps,
+                         a.h0 && a.h0 == a.h_final);
   float* maps = (float*)a.ws;
   const dim3 grid(p.cols, p.segs);
-  cudaError_t err = allow(scan_kernel<T, kZ, false>);
+  auto* run = scan_kernel<T, kZ, false, SPAN>;
+  cudaError_t err = allow(run);
   if (err != cudaSuccess) return err;
   if (p.segs > 1) {
-    if ((err = allow(scan_kernel<T, kZ, true>)) != cudaSuccess) return err;
-    scan_kernel<T, kZ, true><<<grid, p.warps * 32, p.smem, a.stream>>>(a, p.seg_spans, maps);
+    auto* form = scan_kernel<T, kZ, true, SPAN>;
+    if ((err = allow(form)) != cudaSuccess) return err;
+    form<<<grid, p.warps * 32, p.smem, a.stream>>>(a, p.seg_spans, maps);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
   }
-  scan_kernel<T, kZ, false><<<grid, p.warps * 32, p.smem, a.stream>>>(a, p.seg_spans, maps);
+  run<<<grid, p.warps * 32, p.smem, a.stream>>>(a, p.seg_spans, maps);
   return cudaGetLastError();
 }
 
 template <typename T, bool kZ>
 cudaError_t backward_t(const ScanArgs& a) {
+  constexpr int SPAN = sizeof(T) == 2 ? 32 : 64;  // 8 tokens a run
+  using G = Geo<T, SPAN>;
   using E = typename std::conditional<kZ, T, float>::type;
-  const int slot = 2 * (2 * tile_bytes<T, T>() + tile_bytes<T, E>());
-  const Plan p = plan(a, Geo<T>::CB, slot, false);
+  const Plan p =
+      plan<G>(a, kSlots * (2 * tile_bytes<G, T>() + tile_bytes<G, E>()), kWarpsBack, false);
   float* maps = (float*)a.ws;
   float* part = p.segs > 1 ? maps + (size_t)2 * p.segs * a.C : a.dA;
   const dim3 grid(p.cols, p.segs);
-  cudaError_t err = allow(scan_backward_kernel<T, kZ, false>);
+  auto* run = scan_backward_kernel<T, kZ, false, SPAN>;
+  cudaError_t err = allow(run);
   if (err != cudaSuccess) return err;
   if (p.segs > 1) {
-    if ((err = allow(scan_backward_kernel<T, kZ, true>)) != cudaSuccess) return err;
-    scan_backward_kernel<T, kZ, true>
-        <<<grid, p.warps * 32, p.smem, a.stream>>>(a, p.seg_spans, maps, nullptr);
+    auto* form = scan_backward_kernel<T, kZ, true, SPAN>;
+    if ((err = allow(form)) != cudaSuccess) return err;
+    form<<<grid, p.warps * 32, p.smem, a.stream>>>(a, p.seg_spans, maps, nullptr);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
   }
-  scan_backward_kernel<T, kZ, false>
-      <<<grid, p.warps * 32, p.smem, a.stream>>>(a, p.seg_spans, maps, part);
+  run<<<grid, p.warps * 32, p.smem, a.stream>>>(a, p.seg_spans, maps, part);
   if ((err = cudaGetLastError()) != cudaSuccess || !kZ || p.segs == 1) return err;
   sum_rows_kernel<<<(a.C + 63) / 64, 64, 0, a.stream>>>(part, p.segs, a.C, a.dA);
   return cudaGetLastError();
@@ -830,8 +849,8 @@ cudaError_t backward_t(const ScanArgs& a) {
 }  // namespace
 
 size_t scan_workspace_bytes(int T, int C) {
-  const int wide = segments(T, (C + Geo<__nv_bfloat16>::CB - 1) / Geo<__nv_bfloat16>::CB);
-  const int narrow = segments(T, (C + Geo<float>::CB - 1) / Geo<float>::CB);
+  // a block owns 16 channels of bf16, 8 of fp32
+  const int wide = segments(T, (C + 15) / 16), narrow = segments(T, (C + 7) / 8);
   return (size_t)3 * (wide > narrow ? wide : narrow) * C * sizeof(float);
 }
 

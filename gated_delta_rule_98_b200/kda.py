@@ -45,7 +45,7 @@ EXPORTS = ("kda_status_string", "kda_version", "kda_forward_workspace_size",
            "kda_qk_norm_rope_backward")
 
 # Tokens between the states that the gated scan saves for its gradient.
-KDA_SCAN_INTERVAL = 64
+KDA_SCAN_INTERVAL = 32
 
 # Bytes of the library's fixed scratch array used by kda_forward_noalloc.
 KDA_NOALLOC_SCRATCH_BYTES = 64 << 20

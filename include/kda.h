@@ -411,7 +411,7 @@ kda_status kda_short_conv_swish_backward(const void* x, const float* w, const vo
  *  states   : [ceil(T / KDA_SCAN_INTERVAL), channels] float32 or NULL: row j
  *             receives the state entering packed token KDA_SCAN_INTERVAL * j
  *             (unspecified where that token starts a sequence).  The backward
- *             calls need it; it adds 4 bytes per channel to every 64 tokens.
+ *             calls need it; it adds 4 bytes per channel to every 32 tokens.
  *  cu_seqlens, num_seqs, total_tokens, max_seqlen : as in kda_forward, except
  *             that cu_seqlens is not validated (a malformed one gives
  *             undefined values, never an out-of-range access) and
@@ -423,7 +423,7 @@ kda_status kda_short_conv_swish_backward(const void* x, const float* w, const vo
  * The state, the products of a and every sum are float32 in a fixed order
  * (bit-identical from call to call).
  */
-#define KDA_SCAN_INTERVAL 64
+#define KDA_SCAN_INTERVAL 32
 size_t kda_gated_scan_workspace_size(int32_t total_tokens, int32_t channels);
 kda_status kda_gated_scan(const void* x, const void* z, const float* A, const float* h0,
                           const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
