@@ -10,7 +10,11 @@
 // paired with i + rot/2, 8 consecutive channels otherwise.  So a row needs
 // shuffles only for its sums, and a lane needs the sines of four angles
 // whatever the layout.  The sines of a token's rot/2 angles are formed once by
-// the block that owns the token and shared by all its heads.
+// the block that owns the token and shared by all its heads.  The rows of a few
+// tokens' query heads, then of their key heads, are taken two a lane at a time,
+// with the next two on the way meanwhile (one at a time, waiting for loads took
+// 9 of 15 issue slots); the side's weights stay in registers (from shared
+// memory they kept its pipe 80% busy).
 #include "kda_common.cuh"
 #include "kda_launch.h"
 
@@ -19,35 +23,110 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kTokens = 4;  // tokens of one block's step
-constexpr int kMaxBlocks = 148 * 8;
+constexpr int kMaxTokens = 16;  // tokens of one block's step
+constexpr int kRows = 2;        // rows of a lane's batch
+constexpr int kMaxBackBlocks = 148 * 8;
 
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+
+// A lane's eight channels as its four pairs (lo, hi), two pairs a register pair:
+// the halves of every rotated pair lie in lo and in hi.
+struct Row {
+  float2 lo[2], hi[2];
+};
+// The two groups of four channels as they lie in memory, and their pairs:
+// (a[i], b[i]), or neighbours when interleaved.
 template <typename T>
-__device__ __forceinline__ void ld4(const T* p, float* f);
+struct Raw;
 template <>
-__device__ __forceinline__ void ld4<__nv_bfloat16>(const __nv_bfloat16* p, float* f) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  f[0] = __uint_as_float(u.x << 16); f[1] = __uint_as_float(u.x & 0xffff0000u);
-  f[2] = __uint_as_float(u.y << 16); f[3] = __uint_as_float(u.y & 0xffff0000u);
+struct Raw<__nv_bfloat16> {
+  uint2 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, const __nv_bfloat16* q) {
+    a = *reinterpret_cast<const uint2*>(p);
+    b = *reinterpret_cast<const uint2*>(q);
+  }
+  __device__ __forceinline__ void clear() { a = b = make_uint2(0u, 0u); }
+  template <bool kPairs>
+  __device__ __forceinline__ Row get() const {
+    auto l = [](uint32_t u) { return __uint_as_float(u << 16); };
+    auto h = [](uint32_t u) { return __uint_as_float(u & 0xffff0000u); };
+    if (kPairs)
+      return Row{{make_float2(l(a.x), l(a.y)), make_float2(l(b.x), l(b.y))},
+                 {make_float2(h(a.x), h(a.y)), make_float2(h(b.x), h(b.y))}};
+    return Row{{make_float2(l(a.x), h(a.x)), make_float2(l(a.y), h(a.y))},
+               {make_float2(l(b.x), h(b.x)), make_float2(l(b.y), h(b.y))}};
+  }
+};
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p, const float* q) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(q);
+  }
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  template <bool kPairs>
+  __device__ __forceinline__ Row get() const {
+    if (kPairs)
+      return Row{{make_float2(a.x, a.z), make_float2(b.x, b.z)},
+                 {make_float2(a.y, a.w), make_float2(b.y, b.w)}};
+    return Row{{make_float2(a.x, a.y), make_float2(a.z, a.w)},
+               {make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+  }
+};
+// The inverse of Raw::get: the two groups of four channels.
+template <bool kPairs>
+__device__ __forceinline__ void groups_of(const Row& r, float4& a, float4& b) {
+  if (kPairs) {
+    a = make_float4(r.lo[0].x, r.hi[0].x, r.lo[0].y, r.hi[0].y);
+    b = make_float4(r.lo[1].x, r.hi[1].x, r.lo[1].y, r.hi[1].y);
+  } else {
+    a = make_float4(r.lo[0].x, r.lo[0].y, r.lo[1].x, r.lo[1].y);
+    b = make_float4(r.hi[0].x, r.hi[0].y, r.hi[1].x, r.hi[1].y);
+  }
 }
-template <>
-__device__ __forceinline__ void ld4<float>(const float* p, float* f) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-}
-template <typename T>
-__device__ __forceinline__ void st4(T* p, const float* f);
-template <>
-__device__ __forceinline__ void st4<__nv_bfloat16>(__nv_bfloat16* p, const float* f) {
-  __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+__device__ __forceinline__ void st4(__nv_bfloat16* p, float4 f) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(f.x, f.y), b = __floats2bfloat162_rn(f.z, f.w);
   uint2 u;
   u.x = *reinterpret_cast<uint32_t*>(&a);
   u.y = *reinterpret_cast<uint32_t*>(&b);
   *reinterpret_cast<uint2*>(p) = u;
 }
-template <>
-__device__ __forceinline__ void st4<float>(float* p, const float* f) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+__device__ __forceinline__ void st4(float* p, float4 f) { *reinterpret_cast<float4*>(p) = f; }
+
+__device__ __forceinline__ Row mul(const Row& a, const Row& b) {
+  Row r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    r.lo[i] = __fmul2_rn(a.lo[i], b.lo[i]);
+    r.hi[i] = __fmul2_rn(a.hi[i], b.hi[i]);
+  }
+  return r;
+}
+__device__ __forceinline__ Row scale(const Row& a, float f) {
+  Row r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    r.lo[i] = __fmul2_rn(a.lo[i], splat(f));
+    r.hi[i] = __fmul2_rn(a.hi[i], splat(f));
+  }
+  return r;
+}
+__device__ __forceinline__ Row fma(const Row& a, const Row& b, const Row& c) {
+  Row r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    r.lo[i] = __ffma2_rn(a.lo[i], b.lo[i], c.lo[i]);
+    r.hi[i] = __ffma2_rn(a.hi[i], b.hi[i], c.hi[i]);
+  }
+  return r;
+}
+__device__ __forceinline__ float dot(const Row& a, const Row& b) {
+  float2 s = __fmul2_rn(a.lo[0], b.lo[0]);
+  s = __ffma2_rn(a.lo[1], b.lo[1], s);
+  s = __ffma2_rn(a.hi[0], b.hi[0], s);
+  s = __ffma2_rn(a.hi[1], b.hi[1], s);
+  return s.x + s.y;
 }
 
 // Sum over the G lanes of a head row.
@@ -58,113 +137,155 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// Turns the lane's four pairs by (cos, sin); neg: by the opposite angle.
-// Pairs are (v[2i], v[2i+1]) when interleaved, else (v[i], v[4+i]).
-__device__ __forceinline__ void turn(float* v, const float2* cs, bool interleaved, bool neg) {
+// The lane's four pairs turned by the angles with these cosines and sines.
+__device__ __forceinline__ Row turn(const Row& v, const float2 (&c)[2], const float2 (&s)[2]) {
+  Row r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int ia = interleaved ? 2 * i : i, ib = interleaved ? 2 * i + 1 : 4 + i;
-    const float c = cs[i].x, s = neg ? -cs[i].y : cs[i].y;
-    const float x = v[ia], y = v[ib];
-    v[ia] = x * c - y * s;
-    v[ib] = y * c + x * s;
+  for (int i = 0; i < 2; ++i) {
+    const float2 n = __fmul2_rn(s[i], splat(-1.f));
+    r.lo[i] = __ffma2_rn(v.lo[i], c[i], __fmul2_rn(v.hi[i], n));
+    r.hi[i] = __ffma2_rn(v.hi[i], c[i], __fmul2_rn(v.lo[i], s[i]));
   }
+  return r;
 }
 
 template <typename T, int D, bool kPairs, bool kBack>
-__global__ void __launch_bounds__(kThreads) qk_kernel(const QkArgs a, float* part) {
-  constexpr int G = D / 8;             // lanes of a row
-  constexpr int ROWS = kThreads / G;   // rows of a pass
-  __shared__ float2 s_cs[kTokens][D / 2];
-  __shared__ float s_dw[kBack ? 2 : 1][kBack ? ROWS : 1][D];
-  const int l = threadIdx.x % G, row = threadIdx.x / G;
+__global__ void __launch_bounds__(kThreads) qk_kernel(const QkArgs a, int tokens, float* part) {
+  constexpr int G = D / 8;            // lanes of a row
+  constexpr int SLOTS = kThreads / G; // rows of a pass
+  constexpr int U = kRows, BATCH = SLOTS * U;
+  __shared__ __align__(16) float s_cos[kMaxTokens][D / 2], s_sin[kMaxTokens][D / 2];
+  __shared__ __align__(16) float s_dw[kBack ? 2 : 1][kBack ? SLOTS : 1][D];
+  const int l = threadIdx.x % G, slot = threadIdx.x / G;
   const int half = a.rot / 2;
   const bool turned = 8 * l < a.rot;
   const int o1 = !kPairs && turned ? 4 * l : 8 * l;
   const int o2 = !kPairs && turned ? half + 4 * l : 8 * l + 4;
-  float w[2][8], dw[2][8] = {};
+  Row weight[2], dw[2];
 #pragma unroll
-  for (int s = 0; s < 2; ++s)
+  for (int s = 0; s < 2; ++s) {
+    Raw<float> w;
+    w.a = w.b = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (a.side[s].weight) w.load(a.side[s].weight + o1, a.side[s].weight + o2);
+    weight[s] = w.template get<kPairs>();
+    dw[s] = Row{{splat(0.f), splat(0.f)}, {splat(0.f), splat(0.f)}};
+  }
+  const float per_head[2] = {1.f / max(a.side[0].heads, 1), 1.f / max(a.side[1].heads, 1)};
+
+  for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < a.T; t0 += (int64_t)gridDim.x * tokens) {
+    const int count = (int)(a.T - t0 < tokens ? a.T - t0 : tokens);
+    const int nq = (count * a.side[0].heads + BATCH - 1) / BATCH;
+    const int nb = nq + (count * a.side[1].heads + BATCH - 1) / BATCH;
+    Raw<T> x[U], d[kBack ? U : 1];
+    int tok[U], head[U];  // of the rows in x
+    // Batch b's rows; behind the last one zeros, and token -1.
+    auto load = [&](int b) {
+      const int s = b >= nq, heads = a.side[s].heads;
+      const QkSide& q = a.side[s];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      w[s][e] = a.side[s].weight ? a.side[s].weight[o1 + e] : 1.f;
-      w[s][4 + e] = a.side[s].weight ? a.side[s].weight[o2 + e] : 1.f;
-    }
-  for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < a.T; t0 += (int64_t)gridDim.x * kTokens) {
-    const int count = (int)(a.T - t0 < kTokens ? a.T - t0 : kTokens);
-    __syncthreads();
+      for (int u = 0; u < U; ++u) {
+        const int r = (b - (s ? nq : 0)) * BATCH + u * SLOTS + slot;
+        const int k = (int)((r + 0.5f) * per_head[s]);  // r / heads (r is small)
+        const int h = (r - k * heads) * D;
+        tok[u] = r < count * heads ? k : -1;
+        head[u] = h;
+        if (tok[u] >= 0) {
+          const T* p = (const T*)q.x + (t0 + k) * q.x_stride + h;
+          x[u].load(p + o1, p + o2);
+          if (kBack) {
+            const T* g = (const T*)q.dout + (t0 + k) * q.dout_stride + h;
+            d[u].load(g + o1, g + o2);
+          }
+        } else {
+          x[u].clear();
+          if (kBack) d[u].clear();
+        }
+      }
+    };
+    load(0);
+    __syncthreads();  // the last step's sines are read
     for (int i = threadIdx.x; i < count * half; i += kThreads) {
       // in turns, reduced to [-1/2, 1/2] in 64 bits; the rest fits 32
       const double turns = (double)a.positions[t0 + i / half] *
                            (a.freqs[i % half] * 0.15915494309189533577);
-      float s, c;
-      sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-      s_cs[i / half][i % half] = make_float2(c, s);
+      float sn, cn;
+      sincospif(2.f * (float)(turns - rint(turns)), &sn, &cn);
+      s_cos[i / half][i % half] = cn;
+      s_sin[i / half][i % half] = kBack ? -sn : sn;  // the gradient turns back
     }
     __syncthreads();
-    for (int k = 0; k < count; ++k) {
-      float2 cs[4];
+    for (int b = 0; b < nb; ++b) {
+      const bool s = b >= nq;
+      const QkSide& q = a.side[s];
+      Row w, v[U], g[kBack ? U : 1];
+      int k[U], h[U];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) cs[i] = turned ? s_cs[k][4 * l + i] : make_float2(1.f, 0.f);
+      for (int i = 0; i < 2; ++i) {
+        w.lo[i] = s ? weight[1].lo[i] : weight[0].lo[i];
+        w.hi[i] = s ? weight[1].hi[i] : weight[0].hi[i];
+      }
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const QkSide& q = a.side[s];
-        const T* x = (const T*)q.x + (t0 + k) * q.x_stride;
-        T* out = (T*)q.out + (t0 + k) * q.out_stride;
-        for (int h0 = 0; h0 < q.heads; h0 += ROWS) {
-          const int h = h0 + row;
-          const bool in = h < q.heads;
-          float v[8] = {}, b[8] = {};
-          if (in) {
-            ld4<T>(x + h * D + o1, v);
-            ld4<T>(x + h * D + o2, v + 4);
-            if (kBack) {
-              const T* d = (const T*)q.dout + (t0 + k) * q.dout_stride + h * D;
-              ld4<T>(d + o1, b);
-              ld4<T>(d + o2, b + 4);
-            }
+      for (int u = 0; u < U; ++u) {
+        v[u] = x[u].template get<kPairs>();
+        if (kBack) g[u] = d[u].template get<kPairs>();
+        k[u] = tok[u];
+        h[u] = head[u];
+      }
+      if (b + 1 < nb) load(b + 1);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool in = k[u] >= 0;
+        float2 c[2], sn[2];
+        if (turned) {
+          const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[in ? k[u] : 0][4 * l]);
+          const float4 s4 = *reinterpret_cast<const float4*>(&s_sin[in ? k[u] : 0][4 * l]);
+          c[0] = make_float2(c4.x, c4.y);
+          c[1] = make_float2(c4.z, c4.w);
+          sn[0] = make_float2(s4.x, s4.y);
+          sn[1] = make_float2(s4.z, s4.w);
+        }
+        const float rn = rsqrtf(row_sum<G>(dot(v[u], v[u])) * (1.f / D) + a.eps);
+        Row out;
+        if (!kBack) {
+          out = mul(v[u], scale(w, rn));
+          if (turned) out = turn(out, c, sn);
+        } else {
+          Row b_ = g[u];
+          if (turned) b_ = turn(b_, c, sn);
+          const Row vr = scale(v[u], rn);
+          if (in) {  // rn is inf off the rows at eps 0
+            if (s) dw[1] = fma(b_, vr, dw[1]);
+            else dw[0] = fma(b_, vr, dw[0]);
           }
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-          const float r = rsqrtf(row_sum<G>(ss) * (1.f / D) + a.eps);
-          if (!kBack) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= r * w[s][e];
-            if (turned) turn(v, cs, kPairs, false);
-          } else {
-            if (turned) turn(b, cs, kPairs, true);
-            float cv = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (in) dw[s][e] = fmaf(b[e], v[e] * r, dw[s][e]);  // r is inf off the rows at eps 0
-              b[e] *= w[s][e];
-              cv = fmaf(b[e], v[e], cv);
-            }
-            const float m = row_sum<G>(cv) * (1.f / D) * r * r;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = r * (b[e] - v[e] * m);
-          }
-          if (in) {
-            st4<T>(out + h * D + o1, v);
-            st4<T>(out + h * D + o2, v + 4);
-          }
+          b_ = mul(b_, w);
+          // r (c - v r^2 mean(c v)) = r c - (v r) r mean(c (v r))
+          const float m = row_sum<G>(dot(b_, vr)) * (-1.f / D) * rn;
+          Row ms;
+          ms.lo[0] = ms.lo[1] = ms.hi[0] = ms.hi[1] = splat(m);
+          out = fma(vr, ms, scale(b_, rn));
+        }
+        if (in) {
+          float4 f1, f2;
+          groups_of<kPairs>(out, f1, f2);
+          T* p = (T*)q.out + (t0 + k[u]) * q.out_stride + h[u];
+          st4(p + o1, f1);
+          st4(p + o2, f2);
         }
       }
     }
   }
   if (kBack && part) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s_dw[s][row][o1 + e] = dw[s][e];
-        s_dw[s][row][o2 + e] = dw[s][4 + e];
-      }
+    for (int s = 0; s < 2; ++s) {
+      float4 f1, f2;
+      groups_of<kPairs>(dw[s], f1, f2);
+      st4(&s_dw[s][slot][o1], f1);
+      st4(&s_dw[s][slot][o2], f2);
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
       float v = 0.f;
-      for (int r = 0; r < ROWS; ++r) v += s_dw[i / D][r][i % D];
+      for (int r = 0; r < SLOTS; ++r) v += s_dw[i / D][r][i % D];
       part[(size_t)blockIdx.x * 2 * D + i] = v;
     }
   }
@@ -188,21 +309,35 @@ __global__ void __launch_bounds__(128)
   }
 }
 
-int blocks_for(int T) {
-  const int b = (int)(((int64_t)T + kTokens - 1) / kTokens);
-  return b < 1 ? 1 : b > kMaxBlocks ? kMaxBlocks : b;
+// Tokens of a block's step and blocks: one token a step while that fills the GPU
+// no more than twice (the smallest calls are bound by latency); above, four, or
+// more until the smaller side's heads fill a batch; blocks go on in strides.  The
+// gradient's blocks each leave a row of weight sums, so they are fewer.
+void shape_for(const QkArgs& a, bool back, int& tokens, int& blocks) {
+  const int batch = kThreads / (a.d / 8) * kRows;
+  const int hq = a.side[0].heads, hk = a.side[1].heads;
+  const int few = hq < 1 ? hk : hk < 1 || hq < hk ? hq : hk;
+  tokens = 1;
+  if (a.T > 148 * 16) {
+    tokens = 4;
+    while (tokens < kMaxTokens && tokens * few < batch && a.T / tokens > 148 * 16) tokens *= 2;
+  }
+  const int64_t b = ((int64_t)a.T + tokens - 1) / tokens;
+  const int most = back ? kMaxBackBlocks : 148 * 64;
+  blocks = (int)(b < 1 ? 1 : b > most ? most : b);
 }
 
 template <typename T, int D, bool kPairs>
 cudaError_t launch_k(const QkArgs& a, bool back) {
-  const int grid = blocks_for(a.T);
+  int tokens, grid;
+  shape_for(a, back, tokens, grid);
   if (!back) {
-    qk_kernel<T, D, kPairs, false><<<grid, kThreads, 0, a.stream>>>(a, nullptr);
+    qk_kernel<T, D, kPairs, false><<<grid, kThreads, 0, a.stream>>>(a, tokens, nullptr);
     return cudaGetLastError();
   }
   const bool weights = a.side[0].dweight || a.side[1].dweight;
   qk_kernel<T, D, kPairs, true>
-      <<<grid, kThreads, 0, a.stream>>>(a, weights ? (float*)a.ws : nullptr);
+      <<<grid, kThreads, 0, a.stream>>>(a, tokens, weights ? (float*)a.ws : nullptr);
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess || !weights) return err;
   qk_weight_kernel<<<2 * D, 128, 0, a.stream>>>((const float*)a.ws, grid, D, a.side[0].dweight,
@@ -230,7 +365,8 @@ cudaError_t launch(const QkArgs& a, bool back) {
 }  // namespace
 
 size_t qk_backward_workspace_bytes(int T, int d) {
-  return (size_t)blocks_for(T) * 2 * d * sizeof(float);
+  const int blocks = T < 1 ? 1 : T < kMaxBackBlocks ? T : kMaxBackBlocks;
+  return (size_t)blocks * 2 * d * sizeof(float);
 }
 
 cudaError_t launch_qk_norm_rope(const QkArgs& a) { return launch(a, false); }

@@ -723,7 +723,7 @@ def short_conv_swish_backward(x, w, dy, *, cu_seqlens=None, num_seqs=None, max_s
     ws, wsp, nbytes = _workspace_of(
         lib().kda_short_conv_swish_backward_workspace_size(T, C, width), workspace, dev,
         "kda_short_conv_swish_backward_workspace_size")
-    _call(kda_short_conv_swish_backward, dev, stream, xp, wp, dyp, cup, N, T, L, C, width,
+    _call(lib().kda_short_conv_swish_backward, dev, stream, xp, wp, dyp, cup, N, T, L, C, width,
           _dt(x), _role("dx", dx, shape, dt, dev), _role("dw", dw, taps, f32, dev), wsp, nbytes)
     return dx, dw
 
@@ -736,15 +736,16 @@ def _gated_scan(x, z, A, g, h0, cu_seqlens, num_seqs, max_seqlen, y, h_final, st
     xp, h0p = _role("x", x, shape, dt, dev), _role("h0", h0, per_seq, f32, dev)
     cup = _role("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
     if z is None:
-        fn, gate = kda_gated_scan_g, (_role("g", g, shape, f32, dev),)
+        fn, gate = lib().kda_gated_scan_g, (_role("g", g, shape, f32, dev),)
     else:
-        fn, gate = kda_gated_scan, (_role("z", z, shape, dt, dev), _role("A", A, (C,), f32, dev))
+        fn = lib().kda_gated_scan
+        gate = (_role("z", z, shape, dt, dev), _role("A", A, (C,), f32, dev))
     if y is None:
         y = torch.empty_like(x)
     if h_final is None:
-        h_final = torch.empty(per_seq, dtype=f32, device=dev)
+        h_final = x.new_empty(per_seq, dtype=f32)
     if states is None and save_states:
-        states = torch.empty(rows, dtype=f32, device=dev)
+        states = x.new_empty(rows, dtype=f32)
     ws, wsp, nbytes = _workspace_of(lib().kda_gated_scan_workspace_size(T, C), ws, dev,
                                     "kda_gated_scan_workspace_size")
     _call(fn, dev, stream, xp, *gate, h0p, cup, N, T, L, C, _dt(x),
@@ -789,16 +790,16 @@ def _gated_scan_backward(x, z, A, g, states, dy, h0, dh_final, cu_seqlens, num_s
         gp = _role("g", g, shape, f32, dev)
     else:
         zp, Ap = _role("z", z, shape, dt, dev), _role("A", A, (C,), f32, dev)
-    dx, dh0 = torch.empty_like(x), torch.empty(per_seq, dtype=f32, device=dev)
+    dx, dh0 = torch.empty_like(x), x.new_empty(per_seq, dtype=f32)
     ws, wsp, nbytes = _workspace_of(lib().kda_gated_scan_workspace_size(T, C), ws, dev,
                                     "kda_gated_scan_workspace_size")
     if z is None:
         dg = torch.empty_like(g)
-        _call(kda_gated_scan_g_backward, dev, stream, xp, gp, *common, dx.data_ptr(),
+        _call(lib().kda_gated_scan_g_backward, dev, stream, xp, gp, *common, dx.data_ptr(),
               dg.data_ptr(), dh0.data_ptr(), wsp, nbytes)
         return dx, dg, dh0
     dz, dA = torch.empty_like(z), torch.empty_like(A)
-    _call(kda_gated_scan_backward, dev, stream, xp, zp, Ap, *common, dx.data_ptr(),
+    _call(lib().kda_gated_scan_backward, dev, stream, xp, zp, Ap, *common, dx.data_ptr(),
           dz.data_ptr(), dA.data_ptr(), dh0.data_ptr(), wsp, nbytes)
     return dx, dz, dA, dh0
 
@@ -826,7 +827,7 @@ def gated_scan_step(x, z, A, h, *, y=None, stream=None):
     dev, dt, f32, shape = x.device, x.dtype, torch.float32, x.shape
     if y is None:
         y = torch.empty_like(x)
-    _call(kda_gated_scan_step, dev, stream, _role("x", x, shape, dt, dev),
+    _call(lib().kda_gated_scan_step, dev, stream, _role("x", x, shape, dt, dev),
           _role("z", z, shape, dt, dev), _role("A", A, (C,), f32, dev),
           _role("h", h, (B, C), f32, dev), B, C, _dt(x), _role("y", y, shape, dt, dev))
     return y
@@ -842,6 +843,12 @@ def _head_rows(name, t, shape, dtype, device):
     if t.numel() and (sd != 1 or (H > 1 and sh != d)):
         raise ValueError(f"{name}: heads must lie side by side (strides {t.stride()})")
     return t.data_ptr(), (st if T > 1 else H * d)
+
+
+def _new_heads(t):
+    """A contiguous tensor like t [T, heads, d], which may be a slice."""
+    out = torch.empty_like(t)
+    return out if out.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _qk(q, k, positions, freqs, q_weight, k_weight):
@@ -869,10 +876,10 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     T, d, rot, read = _qk(q, k, positions, freqs, q_weight, k_weight)
     dev, dt, qs, ks = q.device, q.dtype, q.shape, k.shape
     if q_out is None:
-        q_out = torch.empty(qs, dtype=dt, device=dev)
+        q_out = _new_heads(q)
     if k_out is None:
-        k_out = torch.empty(ks, dtype=dt, device=dev)
-    _call(kda_qk_norm_rope, dev, stream, *_head_rows("q", q, qs, dt, dev),
+        k_out = _new_heads(k)
+    _call(lib().kda_qk_norm_rope, dev, stream, *_head_rows("q", q, qs, dt, dev),
           *_head_rows("k", k, ks, dt, dev), *read, eps, T, qs[1], ks[1], d, rot,
           1 if interleaved else 0, _dt(q), *_head_rows("q_out", q_out, qs, dt, dev),
           *_head_rows("k_out", k_out, ks, dt, dev))
@@ -889,14 +896,14 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, positions, freqs, *, q_weight=No
     T, d, rot, read = _qk(q, k, positions, freqs, q_weight, k_weight)
     dev, dt, qs, ks = q.device, q.dtype, q.shape, k.shape
     if dq is None:
-        dq = torch.empty(qs, dtype=dt, device=dev)
+        dq = _new_heads(q)
     if dk is None:
-        dk = torch.empty(ks, dtype=dt, device=dev)
+        dk = _new_heads(k)
     dqw = None if q_weight is None else torch.empty_like(q_weight)
     dkw = None if k_weight is None else torch.empty_like(k_weight)
     ws, wsp, nbytes = _workspace_of(lib().kda_qk_norm_rope_backward_workspace_size(T, d),
                                     workspace, dev, "kda_qk_norm_rope_backward_workspace_size")
-    _call(kda_qk_norm_rope_backward, dev, stream, *_head_rows("q", q, qs, dt, dev),
+    _call(lib().kda_qk_norm_rope_backward, dev, stream, *_head_rows("q", q, qs, dt, dev),
           *_head_rows("k", k, ks, dt, dev), *_head_rows("dq_out", dq_out, qs, dt, dev),
           *_head_rows("dk_out", dk_out, ks, dt, dev), *read, eps, T, qs[1], ks[1], d, rot,
           1 if interleaved else 0, _dt(q), *_head_rows("dq", dq, qs, dt, dev),
