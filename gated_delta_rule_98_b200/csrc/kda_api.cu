@@ -187,12 +187,12 @@ kda_status check_qk(const kda::QkArgs& a, kda_dtype dt, bool backward) {
   if (a.rot < 0 || a.rot > a.d || a.rot % 8 != 0) return KDA_ERR_UNSUPPORTED;
   if (a.T < 0 || a.side[0].heads < 0 || a.side[1].heads < 0) return KDA_ERR_INVALID_ARG;
   if (!(a.eps >= 0.f && a.eps <= 3.0e38f)) return KDA_ERR_INVALID_ARG;
+  if (((int64_t)a.side[0].heads + a.side[1].heads) * a.d > 1 << 20) return KDA_ERR_UNSUPPORTED;
   bool work = false;
   for (const kda::QkSide& s : a.side) {
     const bool w = a.T > 0 && s.heads > 0;
     const int64_t row = (int64_t)s.heads * a.d;
     work = work || w;
-    if (row > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
     if (!qk_tensor_ok(w, s.x, s.x_stride, row) || !qk_tensor_ok(w, s.out, s.out_stride, row) ||
         (backward && !qk_tensor_ok(w, s.dout, s.dout_stride, row)) || !opt_aligned16(s.weight) ||
         !opt_aligned4(s.dweight))

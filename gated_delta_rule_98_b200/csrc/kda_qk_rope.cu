@@ -10,11 +10,11 @@
 // paired with i + rot/2, 8 consecutive channels otherwise.  So a row needs
 // shuffles only for its sums, and a lane needs the sines of four angles
 // whatever the layout.  The sines of a token's rot/2 angles are formed once by
-// the block that owns the token and shared by all its heads.  The rows of a few
-// tokens' query heads, then of their key heads, are taken two a lane at a time,
-// with the next two on the way meanwhile (one at a time, waiting for loads took
-// 9 of 15 issue slots); the side's weights stay in registers (from shared
-// memory they kept its pipe 80% busy).
+// the block that owns the token and shared by all its heads.  A lane group goes
+// along the heads of one token, two of q and two of k at a time (one row at a
+// time, waiting for loads took 9 of 15 issue slots), so that weights and sines
+// are fixed while it does and a row costs few instructions besides its
+// arithmetic; the many resident blocks hide the rest.
 #include "kda_common.cuh"
 #include "kda_launch.h"
 
@@ -23,9 +23,9 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kMaxTokens = 16;  // tokens of one block's step
+constexpr int kMaxTokens = 16;  // tokens of a block's step
 constexpr int kRows = 2;        // rows of a lane's batch
-constexpr int kMaxBackBlocks = 148 * 8;
+constexpr int kMaxBlocks = 148 * 8;  // of the gradient: each leaves a row of weight sums
 
 __device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
 
@@ -149,13 +149,116 @@ __device__ __forceinline__ Row turn(const Row& v, const float2 (&c)[2], const fl
   return r;
 }
 
-template <typename T, int D, bool kPairs, bool kBack>
-__global__ void __launch_bounds__(kThreads) qk_kernel(const QkArgs a, int tokens, float* part) {
+// across: lane groups along the heads (a power of two); the others take other tokens.
+template <typename T, int D, bool kPairs>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 5)
+    qk_kernel(const QkArgs a, int tokens, int across) {
+  constexpr int G = D / 8;            // lanes of a row
+  constexpr int SLOTS = kThreads / G; // rows of a pass
+  constexpr int U = kRows;
+  __shared__ __align__(16) float s_cos[kMaxTokens][D / 2], s_sin[kMaxTokens][D / 2];
+  __shared__ double s_freq[D / 2];  // turns per position
+  const int l = threadIdx.x % G, slot = threadIdx.x / G;
+  const int half = a.rot / 2;
+  const bool turned = 8 * l < a.rot;
+  const int o1 = !kPairs && turned ? 4 * l : 8 * l;
+  const int o2 = (!kPairs && turned ? half + 4 * l : 8 * l + 4) - o1;
+  const int lane_token = slot / across, lane_head = slot % across, side_by_side = SLOTS / across;
+  const int most = max(a.side[0].heads, a.side[1].heads);
+  Row weight[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    Raw<float> w;
+    w.a = w.b = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (a.side[s].weight) w.load(a.side[s].weight + o1, a.side[s].weight + o1 + o2);
+    weight[s] = w.template get<kPairs>();
+  }
+  for (int i = threadIdx.x; i < half; i += kThreads) s_freq[i] = a.freqs[i] * 0.15915494309189533577;
+
+  for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < a.T; t0 += (int64_t)gridDim.x * tokens) {
+    const int count = (int)(a.T - t0 < tokens ? a.T - t0 : tokens);
+    __syncthreads();  // the last step's sines are read
+    for (int i = threadIdx.x; i < count * half; i += kThreads) {
+      // in turns, reduced to [-1/2, 1/2] in 64 bits; the rest fits 32
+      const int k = i / half, f = i - k * half;
+      const double turns = (double)a.positions[t0 + k] * s_freq[f];
+      float sn, cn;
+      sincospif(2.f * (float)(turns - rint(turns)), &sn, &cn);
+      s_cos[k][f] = cn;
+      s_sin[k][f] = sn;
+    }
+    __syncthreads();
+    for (int k0 = 0; k0 < count; k0 += side_by_side) {
+      const int k = k0 + lane_token;
+      const bool here = k < count;
+      const int64_t t = t0 + (here ? k : 0);
+      float2 c[2], sn[2];
+      if (turned) {
+        const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[here ? k : 0][4 * l]);
+        const float4 s4 = *reinterpret_cast<const float4*>(&s_sin[here ? k : 0][4 * l]);
+        c[0] = make_float2(c4.x, c4.y);
+        c[1] = make_float2(c4.z, c4.w);
+        sn[0] = make_float2(s4.x, s4.y);
+        sn[1] = make_float2(s4.z, s4.w);
+      }
+      // this lane group's first head of either side; offsets of its rows from there
+      const T* px[2];
+      T* po[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const QkSide& q = a.side[s];
+        px[s] = (const T*)q.x + t * q.x_stride + lane_head * D + o1;
+        po[s] = (T*)q.out + t * q.out_stride + lane_head * D + o1;
+      }
+      for (int h0 = 0; h0 < most; h0 += across * U) {
+        Raw<T> x[2][U];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int h = h0 + u * across;
+            if (here && h + lane_head < a.side[s].heads) {
+              x[s][u].load(px[s] + h * D, px[s] + h * D + o2);
+            } else {
+              x[s][u].clear();
+            }
+          }
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int h = h0 + u * across;
+            if (h >= a.side[s].heads) break;
+            const bool in = here && h + lane_head < a.side[s].heads;
+            const Row v = x[s][u].template get<kPairs>();
+            const float rn = rsqrtf(row_sum<G>(dot(v, v)) * (1.f / D) + a.eps);
+            Row out = mul(v, scale(weight[s], rn));
+            if (turned) out = turn(out, c, sn);
+            if (in) {
+              float4 f1, f2;
+              groups_of<kPairs>(out, f1, f2);
+              st4(po[s] + h * D, f1);
+              st4(po[s] + h * D + o2, f2);
+            }
+          }
+      }
+    }
+  }
+}
+
+// The gradient deals rows out freely, first the step's query heads, then its key
+// heads, each with its own token and head, the next two on the way while two are
+// worked on: more instructions a row than the forward's walk, but its two inputs
+// a row and its weight sums leave too few resident warps to hide the loads
+// otherwise (16384 x (16 + 16) x 128: 94 us; walking as the forward does, 106).
+template <typename T, int D, bool kPairs>
+__global__ void __launch_bounds__(kThreads)
+    qk_backward_kernel(const QkArgs a, int tokens, float* part) {
   constexpr int G = D / 8;            // lanes of a row
   constexpr int SLOTS = kThreads / G; // rows of a pass
   constexpr int U = kRows, BATCH = SLOTS * U;
   __shared__ __align__(16) float s_cos[kMaxTokens][D / 2], s_sin[kMaxTokens][D / 2];
-  __shared__ __align__(16) float s_dw[kBack ? 2 : 1][kBack ? SLOTS : 1][D];
+  __shared__ __align__(16) float s_dw[2][SLOTS][D];
   const int l = threadIdx.x % G, slot = threadIdx.x / G;
   const int half = a.rot / 2;
   const bool turned = 8 * l < a.rot;
@@ -176,7 +279,7 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const QkArgs a, int tokens
     const int count = (int)(a.T - t0 < tokens ? a.T - t0 : tokens);
     const int nq = (count * a.side[0].heads + BATCH - 1) / BATCH;
     const int nb = nq + (count * a.side[1].heads + BATCH - 1) / BATCH;
-    Raw<T> x[U], d[kBack ? U : 1];
+    Raw<T> x[U], d[U];
     int tok[U], head[U];  // of the rows in x
     // Batch b's rows; behind the last one zeros, and token -1.
     auto load = [&](int b) {
@@ -185,20 +288,19 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const QkArgs a, int tokens
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int r = (b - (s ? nq : 0)) * BATCH + u * SLOTS + slot;
-        const int k = (int)((r + 0.5f) * per_head[s]);  // r / heads (r is small)
+        // r / heads, exactly: r < 16 heads + a batch stays below 2^20
+        const int k = (int)((r + 0.5f) * per_head[s]);
         const int h = (r - k * heads) * D;
         tok[u] = r < count * heads ? k : -1;
         head[u] = h;
         if (tok[u] >= 0) {
           const T* p = (const T*)q.x + (t0 + k) * q.x_stride + h;
           x[u].load(p + o1, p + o2);
-          if (kBack) {
-            const T* g = (const T*)q.dout + (t0 + k) * q.dout_stride + h;
-            d[u].load(g + o1, g + o2);
-          }
+          const T* g = (const T*)q.dout + (t0 + k) * q.dout_stride + h;
+          d[u].load(g + o1, g + o2);
         } else {
           x[u].clear();
-          if (kBack) d[u].clear();
+          d[u].clear();
         }
       }
     };
@@ -211,13 +313,13 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const QkArgs a, int tokens
       float sn, cn;
       sincospif(2.f * (float)(turns - rint(turns)), &sn, &cn);
       s_cos[i / half][i % half] = cn;
-      s_sin[i / half][i % half] = kBack ? -sn : sn;  // the gradient turns back
+      s_sin[i / half][i % half] = -sn;  // the gradient turns back
     }
     __syncthreads();
     for (int b = 0; b < nb; ++b) {
       const bool s = b >= nq;
       const QkSide& q = a.side[s];
-      Row w, v[U], g[kBack ? U : 1];
+      Row w, v[U], g[U];
       int k[U], h[U];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -227,7 +329,7 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const QkArgs a, int tokens
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         v[u] = x[u].template get<kPairs>();
-        if (kBack) g[u] = d[u].template get<kPairs>();
+        g[u] = d[u].template get<kPairs>();
         k[u] = tok[u];
         h[u] = head[u];
       }
@@ -245,25 +347,19 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const QkArgs a, int tokens
           sn[1] = make_float2(s4.z, s4.w);
         }
         const float rn = rsqrtf(row_sum<G>(dot(v[u], v[u])) * (1.f / D) + a.eps);
-        Row out;
-        if (!kBack) {
-          out = mul(v[u], scale(w, rn));
-          if (turned) out = turn(out, c, sn);
-        } else {
-          Row b_ = g[u];
-          if (turned) b_ = turn(b_, c, sn);
-          const Row vr = scale(v[u], rn);
-          if (in) {  // rn is inf off the rows at eps 0
-            if (s) dw[1] = fma(b_, vr, dw[1]);
-            else dw[0] = fma(b_, vr, dw[0]);
-          }
-          b_ = mul(b_, w);
-          // r (c - v r^2 mean(c v)) = r c - (v r) r mean(c (v r))
-          const float m = row_sum<G>(dot(b_, vr)) * (-1.f / D) * rn;
-          Row ms;
-          ms.lo[0] = ms.lo[1] = ms.hi[0] = ms.hi[1] = splat(m);
-          out = fma(vr, ms, scale(b_, rn));
+        Row b_ = g[u];
+        if (turned) b_ = turn(b_, c, sn);
+        const Row vr = scale(v[u], rn);
+        if (in) {  // rn is inf off the rows at eps 0
+          if (s) dw[1] = fma(b_, vr, dw[1]);
+          else dw[0] = fma(b_, vr, dw[0]);
         }
+        b_ = mul(b_, w);
+        // r (c - v r^2 mean(c v)) = r c - (v r) r mean(c (v r))
+        const float m = row_sum<G>(dot(b_, vr)) * (-1.f / D) * rn;
+        Row ms;
+        ms.lo[0] = ms.lo[1] = ms.hi[0] = ms.hi[1] = splat(m);
+        const Row out = fma(vr, ms, scale(b_, rn));
         if (in) {
           float4 f1, f2;
           groups_of<kPairs>(out, f1, f2);
@@ -274,7 +370,7 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const QkArgs a, int tokens
       }
     }
   }
-  if (kBack && part) {
+  if (part) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       float4 f1, f2;
@@ -309,39 +405,43 @@ __global__ void __launch_bounds__(128)
   }
 }
 
-// Tokens of a block's step and blocks: one token a step while that fills the GPU
-// no more than twice (the smallest calls are bound by latency); above, four, or
-// more until the smaller side's heads fill a batch; blocks go on in strides.  The
-// gradient's blocks each leave a row of weight sums, so they are fewer.
-void shape_for(const QkArgs& a, bool back, int& tokens, int& blocks) {
-  const int batch = kThreads / (a.d / 8) * kRows;
-  const int hq = a.side[0].heads, hk = a.side[1].heads;
-  const int few = hq < 1 ? hk : hk < 1 || hq < hk ? hq : hk;
+// Tokens of a block's step and blocks.  One token a step while that fills the GPU
+// no more than twice (the smallest calls are bound by latency); above, four (the
+// sines of four tokens are formed in one go) or `enough`.  Blocks go on in strides.
+void steps_for(int T, int enough, int most_blocks, int& tokens, int& blocks) {
   tokens = 1;
-  if (a.T > 148 * 16) {
+  if (T > 148 * 16) {
     tokens = 4;
-    while (tokens < kMaxTokens && tokens * few < batch && a.T / tokens > 148 * 16) tokens *= 2;
+    while (tokens < kMaxTokens && tokens < enough) tokens *= 2;
   }
-  const int64_t b = ((int64_t)a.T + tokens - 1) / tokens;
-  const int most = back ? kMaxBackBlocks : 148 * 64;
-  blocks = (int)(b < 1 ? 1 : b > most ? most : b);
+  const int64_t b = ((int64_t)T + tokens - 1) / tokens;
+  blocks = (int)(b < 1 ? 1 : b > most_blocks ? most_blocks : b);
 }
 
 template <typename T, int D, bool kPairs>
 cudaError_t launch_k(const QkArgs& a, bool back) {
-  int tokens, grid;
-  shape_for(a, back, tokens, grid);
+  constexpr int SLOTS = kThreads / (D / 8);
+  const int hq = a.side[0].heads, hk = a.side[1].heads;
+  int tokens, blocks;
   if (!back) {
-    qk_kernel<T, D, kPairs, false><<<grid, kThreads, 0, a.stream>>>(a, tokens, nullptr);
+    // lane groups along the heads: two heads of the larger side each, up to the
+    // block's; the others take tokens side by side
+    int across = 1;
+    while (across * kRows < (hq > hk ? hq : hk) && across < SLOTS) across *= 2;
+    steps_for(a.T, SLOTS / across, 148 * 64, tokens, blocks);
+    qk_kernel<T, D, kPairs><<<blocks, kThreads, 0, a.stream>>>(a, tokens, across);
     return cudaGetLastError();
   }
+  // tokens until the smaller side's heads fill a batch
+  const int few = hq < 1 ? hk : hk < 1 || hq < hk ? hq : hk;
+  steps_for(a.T, (SLOTS * kRows + few - 1) / (few < 1 ? 1 : few), kMaxBlocks, tokens, blocks);
   const bool weights = a.side[0].dweight || a.side[1].dweight;
-  qk_kernel<T, D, kPairs, true>
-      <<<grid, kThreads, 0, a.stream>>>(a, tokens, weights ? (float*)a.ws : nullptr);
+  qk_backward_kernel<T, D, kPairs>
+      <<<blocks, kThreads, 0, a.stream>>>(a, tokens, weights ? (float*)a.ws : nullptr);
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess || !weights) return err;
-  qk_weight_kernel<<<2 * D, 128, 0, a.stream>>>((const float*)a.ws, grid, D, a.side[0].dweight,
-                                                a.side[1].dweight);
+  qk_weight_kernel<<<2 * D, 128, 0, a.stream>>>((const float*)a.ws, blocks, D,
+                                                a.side[0].dweight, a.side[1].dweight);
   return cudaGetLastError();
 }
 
@@ -365,7 +465,7 @@ cudaError_t launch(const QkArgs& a, bool back) {
 }  // namespace
 
 size_t qk_backward_workspace_bytes(int T, int d) {
-  const int blocks = T < 1 ? 1 : T < kMaxBackBlocks ? T : kMaxBackBlocks;
+  const int blocks = T < 1 ? 1 : T < kMaxBlocks ? T : kMaxBlocks;
   return (size_t)blocks * 2 * d * sizeof(float);
 }
 

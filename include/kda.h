@@ -514,7 +514,8 @@ kda_status kda_gated_scan_step(const void* x, const void* z, const float* A, flo
  *             NULL when rot is 0).
  *  q_weight, k_weight : [d] float32 gains, 16-byte aligned, or NULL (ones).
  *  eps      : finite, not negative.
- *  T >= 0; Hq, Hk >= 0 (a side with no heads may be NULL); d in {32, 64, 128};
+ *  T >= 0; Hq, Hk >= 0 (a side with no heads may be NULL), (Hq + Hk) * d at
+ *  most 2^20; d in {32, 64, 128};
  *  rot a multiple of 8, 0 <= rot <= d (else KDA_ERR_UNSUPPORTED).
  * One launch; no workspace.  Decode is T = B tokens.
  */
