@@ -660,31 +660,31 @@ def _packed(x, cu_seqlens, num_seqs, max_seqlen):
 
 
 def _role(name, t, shape, dtype, device):
-    """Raise ValueError unless t is on ``device``, contiguous, and of its role's
-    shape and dtype.  Returns its address (None for None)."""
+    """Raise ValueError unless t is on the GPU of index ``device``, contiguous, and
+    of its role's shape and dtype.  Returns its address (None for None)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected contiguous "
-                         f"{tuple(shape)} {dtype} on {device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected contiguous "
+                     f"{tuple(shape)} {dtype} on the GPU of the first tensor")
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _call(fn, device, stream, *args):
-    """Run a C entry point on the tensors' device and its current stream (or
-    ``stream``), and raise unless it returns KDA_OK."""
-    if device.type != "cuda":
+    """Run a C entry point on GPU ``device`` and its current stream (or ``stream``),
+    and raise unless it returns KDA_OK."""
+    if device < 0:
         raise ValueError("KDA runs on the GPU only: pass CUDA tensors")
     if stream is not None:
         stream = stream.cuda_stream
     elif _raw_stream is not None:
-        stream = _raw_stream(device.index)
+        stream = _raw_stream(device)
     else:
         stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
+    if device == torch.cuda.current_device():
         st = fn(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -693,15 +693,16 @@ def _call(fn, device, stream, *args):
         raise KdaError(st, fn.__name__)
 
 
-def _workspace_of(nbytes, ws, device, what):
+def _workspace_of(nbytes, ws, like, what):
     """(tensor, address, bytes) of a call's workspace; the caller keeps the tensor
     until it has enqueued its work."""
     if nbytes == 0:
         raise KdaError(KDA_ERR_UNSUPPORTED, what)
     if ws is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    elif ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"workspace: contiguous uint8 on {device} expected")
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return ws, ws.data_ptr(), nbytes
+    if ws.dtype != torch.uint8 or ws.get_device() != like.get_device() or not ws.is_contiguous():
+        raise ValueError(f"workspace: contiguous uint8 on {like.device} expected")
     return ws, ws.data_ptr(), ws.numel()
 
 
@@ -712,7 +713,7 @@ def short_conv_swish_backward(x, w, dy, *, cu_seqlens=None, num_seqs=None, max_s
     cu_seqlens[N] on (a padded batch) are left as they were in dx."""
     T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
     width = w.shape[-1]
-    dev, dt, f32, shape, taps = x.device, x.dtype, torch.float32, x.shape, (C, width)
+    dev, dt, f32, shape, taps = x.get_device(), x.dtype, torch.float32, x.shape, (C, width)
     xp, wp = _role("x", x, shape, dt, dev), _role("w", w, taps, f32, dev)
     dyp = _role("dy", dy, shape, dt, dev)
     cup = _role("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
@@ -721,7 +722,7 @@ def short_conv_swish_backward(x, w, dy, *, cu_seqlens=None, num_seqs=None, max_s
     if dw is None:
         dw = torch.empty_like(w)
     ws, wsp, nbytes = _workspace_of(
-        lib().kda_short_conv_swish_backward_workspace_size(T, C, width), workspace, dev,
+        lib().kda_short_conv_swish_backward_workspace_size(T, C, width), workspace, x,
         "kda_short_conv_swish_backward_workspace_size")
     _call(lib().kda_short_conv_swish_backward, dev, stream, xp, wp, dyp, cup, N, T, L, C, width,
           _dt(x), _role("dx", dx, shape, dt, dev), _role("dw", dw, taps, f32, dev), wsp, nbytes)
@@ -731,7 +732,7 @@ def short_conv_swish_backward(x, w, dy, *, cu_seqlens=None, num_seqs=None, max_s
 def _gated_scan(x, z, A, g, h0, cu_seqlens, num_seqs, max_seqlen, y, h_final, states,
                 save_states, ws, stream):
     T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
-    dev, dt, f32, shape, per_seq = x.device, x.dtype, torch.float32, x.shape, (N, C)
+    dev, dt, f32, shape, per_seq = x.get_device(), x.dtype, torch.float32, x.shape, (N, C)
     rows = ((T + KDA_SCAN_INTERVAL - 1) // KDA_SCAN_INTERVAL, C)
     xp, h0p = _role("x", x, shape, dt, dev), _role("h0", h0, per_seq, f32, dev)
     cup = _role("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
@@ -743,10 +744,10 @@ def _gated_scan(x, z, A, g, h0, cu_seqlens, num_seqs, max_seqlen, y, h_final, st
     if y is None:
         y = torch.empty_like(x)
     if h_final is None:
-        h_final = x.new_empty(per_seq, dtype=f32)
+        h_final = x.new_empty(per_seq, dtype=f32) if h0 is None else torch.empty_like(h0)
     if states is None and save_states:
         states = x.new_empty(rows, dtype=f32)
-    ws, wsp, nbytes = _workspace_of(lib().kda_gated_scan_workspace_size(T, C), ws, dev,
+    ws, wsp, nbytes = _workspace_of(lib().kda_gated_scan_workspace_size(T, C), ws, x,
                                     "kda_gated_scan_workspace_size")
     _call(fn, dev, stream, xp, *gate, h0p, cup, N, T, L, C, _dt(x),
           _role("y", y, shape, dt, dev), _role("h_final", h_final, per_seq, f32, dev),
@@ -780,7 +781,7 @@ def gated_scan_g(x, g, *, h0=None, cu_seqlens=None, num_seqs=None, max_seqlen=No
 def _gated_scan_backward(x, z, A, g, states, dy, h0, dh_final, cu_seqlens, num_seqs, max_seqlen,
                          ws, stream):
     T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
-    dev, dt, f32, shape, per_seq = x.device, x.dtype, torch.float32, x.shape, (N, C)
+    dev, dt, f32, shape, per_seq = x.get_device(), x.dtype, torch.float32, x.shape, (N, C)
     rows = ((T + KDA_SCAN_INTERVAL - 1) // KDA_SCAN_INTERVAL, C)
     xp = _role("x", x, shape, dt, dev)
     common = (_role("states", states, rows, f32, dev), _role("h0", h0, per_seq, f32, dev),
@@ -790,8 +791,9 @@ def _gated_scan_backward(x, z, A, g, states, dy, h0, dh_final, cu_seqlens, num_s
         gp = _role("g", g, shape, f32, dev)
     else:
         zp, Ap = _role("z", z, shape, dt, dev), _role("A", A, (C,), f32, dev)
-    dx, dh0 = torch.empty_like(x), x.new_empty(per_seq, dtype=f32)
-    ws, wsp, nbytes = _workspace_of(lib().kda_gated_scan_workspace_size(T, C), ws, dev,
+    dx, like = torch.empty_like(x), h0 if dh_final is None else dh_final
+    dh0 = x.new_empty(per_seq, dtype=f32) if like is None else torch.empty_like(like)
+    ws, wsp, nbytes = _workspace_of(lib().kda_gated_scan_workspace_size(T, C), ws, x,
                                     "kda_gated_scan_workspace_size")
     if z is None:
         dg = torch.empty_like(g)
@@ -824,7 +826,7 @@ def gated_scan_step(x, z, A, h, *, y=None, stream=None):
     """One step of gated_scan for B sequences: x, z [B, ...], A [channels] fp32;
     h [B, channels] fp32 is updated in place.  Returns y (x's shape and dtype)."""
     B, C, _, _ = _packed(x, None, 1, None)
-    dev, dt, f32, shape = x.device, x.dtype, torch.float32, x.shape
+    dev, dt, f32, shape = x.get_device(), x.dtype, torch.float32, x.shape
     if y is None:
         y = torch.empty_like(x)
     _call(lib().kda_gated_scan_step, dev, stream, _role("x", x, shape, dt, dev),
@@ -835,12 +837,12 @@ def gated_scan_step(x, z, A, h, *, y=None, stream=None):
 
 def _head_rows(name, t, shape, dtype, device):
     """(address, token stride) of a [T, heads, d] tensor whose heads lie side by side."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
         raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected "
-                         f"{tuple(shape)} {dtype} on {device}")
+                         f"{tuple(shape)} {dtype} on the GPU of the first tensor")
     T, H, d = shape
     st, sh, sd = t.stride()
-    if t.numel() and (sd != 1 or (H > 1 and sh != d)):
+    if T * H and (sd != 1 or (H > 1 and sh != d)):
         raise ValueError(f"{name}: heads must lie side by side (strides {t.stride()})")
     return t.data_ptr(), (st if T > 1 else H * d)
 
@@ -853,7 +855,7 @@ def _new_heads(t):
 
 def _qk(q, k, positions, freqs, q_weight, k_weight):
     """(T, d, rot) and the addresses of what both directions read besides q and k."""
-    dev, f32 = q.device, torch.float32
+    dev, f32 = q.get_device(), torch.float32
     if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
         raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}: [T, Hq, d] and [T, Hk, d] "
                          "expected")
@@ -874,7 +876,7 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     k may be slices of one projection's output (heads side by side, any token
     stride); q_out = q, k_out = k works in place.  Returns (q_out, k_out)."""
     T, d, rot, read = _qk(q, k, positions, freqs, q_weight, k_weight)
-    dev, dt, qs, ks = q.device, q.dtype, q.shape, k.shape
+    dev, dt, qs, ks = q.get_device(), q.dtype, q.shape, k.shape
     if q_out is None:
         q_out = _new_heads(q)
     if k_out is None:
@@ -894,7 +896,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, positions, freqs, *, q_weight=No
     (dq, dk, dq_weight, dk_weight), the last two [d] fp32 or None where the
     gain is None."""
     T, d, rot, read = _qk(q, k, positions, freqs, q_weight, k_weight)
-    dev, dt, qs, ks = q.device, q.dtype, q.shape, k.shape
+    dev, dt, qs, ks = q.get_device(), q.dtype, q.shape, k.shape
     if dq is None:
         dq = _new_heads(q)
     if dk is None:
@@ -902,7 +904,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, positions, freqs, *, q_weight=No
     dqw = None if q_weight is None else torch.empty_like(q_weight)
     dkw = None if k_weight is None else torch.empty_like(k_weight)
     ws, wsp, nbytes = _workspace_of(lib().kda_qk_norm_rope_backward_workspace_size(T, d),
-                                    workspace, dev, "kda_qk_norm_rope_backward_workspace_size")
+                                    workspace, q, "kda_qk_norm_rope_backward_workspace_size")
     _call(lib().kda_qk_norm_rope_backward, dev, stream, *_head_rows("q", q, qs, dt, dev),
           *_head_rows("k", k, ks, dt, dev), *_head_rows("dq_out", dq_out, qs, dt, dev),
           *_head_rows("dk_out", dk_out, ks, dt, dev), *read, eps, T, qs[1], ks[1], d, rot,
