@@ -465,6 +465,8 @@ kda_status kda_short_conv_swish_backward(const void* x, const float* w, const vo
   if (width < 1 || width > 4) return KDA_ERR_UNSUPPORTED;
   if (channels < 8 || channels % 8 != 0) return KDA_ERR_UNSUPPORTED;
   if (num_seqs < 0 || total_tokens < 0 || max_seqlen < 0) return KDA_ERR_INVALID_ARG;
+  // the kernel's token arithmetic is 32-bit (offsets are 64-bit)
+  if (total_tokens > 0x7fffff00) return KDA_ERR_UNSUPPORTED;
   if (!cu_seqlens && (int64_t)num_seqs * max_seqlen != total_tokens) return KDA_ERR_INVALID_ARG;
   if (total_tokens > 0 && num_seqs == 0) return KDA_ERR_INVALID_ARG;
   if (!w || !dw || !opt_aligned4(w) || !opt_aligned4(dw) || !opt_aligned4(cu_seqlens))

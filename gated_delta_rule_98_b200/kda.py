@@ -673,14 +673,16 @@ def _role(name, t, shape, dtype, device):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _call(fn, device, stream, *args):
-    """Run a C entry point on GPU ``device`` and its current stream (or ``stream``),
-    and raise unless it returns KDA_OK."""
+# The helpers below run on ``stream`` by making it current, so that the outputs and
+# workspaces they allocate belong to it (a freed workspace could otherwise be handed
+# out again while the kernels still use it).
+
+def _call(fn, device, *args):
+    """Run a C entry point on GPU ``device`` and its current stream, and raise
+    unless it returns KDA_OK."""
     if device < 0:
         raise ValueError("KDA runs on the GPU only: pass CUDA tensors")
-    if stream is not None:
-        stream = stream.cuda_stream
-    elif _raw_stream is not None:
+    if _raw_stream is not None:
         stream = _raw_stream(device)
     else:
         stream = torch.cuda.current_stream(device).cuda_stream
@@ -711,6 +713,11 @@ def short_conv_swish_backward(x, w, dy, *, cu_seqlens=None, num_seqs=None, max_s
     """Gradient of short_conv_swish: dy is the gradient of y (x's shape and
     dtype).  Returns (dx, dw), dw [channels, width] fp32.  Rows from
     cu_seqlens[N] on (a padded batch) are left as they were in dx."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return short_conv_swish_backward(x, w, dy, cu_seqlens=cu_seqlens, num_seqs=num_seqs,
+                                             max_seqlen=max_seqlen, dx=dx, dw=dw,
+                                             workspace=workspace)
     T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
     width = w.shape[-1]
     dev, dt, f32, shape, taps = x.get_device(), x.dtype, torch.float32, x.shape, (C, width)
@@ -724,13 +731,17 @@ def short_conv_swish_backward(x, w, dy, *, cu_seqlens=None, num_seqs=None, max_s
     ws, wsp, nbytes = _workspace_of(
         lib().kda_short_conv_swish_backward_workspace_size(T, C, width), workspace, x,
         "kda_short_conv_swish_backward_workspace_size")
-    _call(lib().kda_short_conv_swish_backward, dev, stream, xp, wp, dyp, cup, N, T, L, C, width,
+    _call(lib().kda_short_conv_swish_backward, dev, xp, wp, dyp, cup, N, T, L, C, width,
           _dt(x), _role("dx", dx, shape, dt, dev), _role("dw", dw, taps, f32, dev), wsp, nbytes)
     return dx, dw
 
 
 def _gated_scan(x, z, A, g, h0, cu_seqlens, num_seqs, max_seqlen, y, h_final, states,
                 save_states, ws, stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _gated_scan(x, z, A, g, h0, cu_seqlens, num_seqs, max_seqlen, y, h_final,
+                               states, save_states, ws, None)
     T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
     dev, dt, f32, shape, per_seq = x.get_device(), x.dtype, torch.float32, x.shape, (N, C)
     rows = ((T + KDA_SCAN_INTERVAL - 1) // KDA_SCAN_INTERVAL, C)
@@ -744,12 +755,12 @@ def _gated_scan(x, z, A, g, h0, cu_seqlens, num_seqs, max_seqlen, y, h_final, st
     if y is None:
         y = torch.empty_like(x)
     if h_final is None:
-        h_final = x.new_empty(per_seq, dtype=f32) if h0 is None else torch.empty_like(h0)
+        h_final = (A if g is None else g).new_empty(N, C)
     if states is None and save_states:
-        states = x.new_empty(rows, dtype=f32)
+        states = (A if g is None else g).new_empty(*rows)
     ws, wsp, nbytes = _workspace_of(lib().kda_gated_scan_workspace_size(T, C), ws, x,
                                     "kda_gated_scan_workspace_size")
-    _call(fn, dev, stream, xp, *gate, h0p, cup, N, T, L, C, _dt(x),
+    _call(fn, dev, xp, *gate, h0p, cup, N, T, L, C, _dt(x),
           _role("y", y, shape, dt, dev), _role("h_final", h_final, per_seq, f32, dev),
           _role("states", states, rows, f32, dev), wsp, nbytes)
     return (y, h_final) if states is None else (y, h_final, states)
@@ -780,6 +791,10 @@ def gated_scan_g(x, g, *, h0=None, cu_seqlens=None, num_seqs=None, max_seqlen=No
 
 def _gated_scan_backward(x, z, A, g, states, dy, h0, dh_final, cu_seqlens, num_seqs, max_seqlen,
                          ws, stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _gated_scan_backward(x, z, A, g, states, dy, h0, dh_final, cu_seqlens,
+                                        num_seqs, max_seqlen, ws, None)
     T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
     dev, dt, f32, shape, per_seq = x.get_device(), x.dtype, torch.float32, x.shape, (N, C)
     rows = ((T + KDA_SCAN_INTERVAL - 1) // KDA_SCAN_INTERVAL, C)
@@ -791,17 +806,16 @@ def _gated_scan_backward(x, z, A, g, states, dy, h0, dh_final, cu_seqlens, num_s
         gp = _role("g", g, shape, f32, dev)
     else:
         zp, Ap = _role("z", z, shape, dt, dev), _role("A", A, (C,), f32, dev)
-    dx, like = torch.empty_like(x), h0 if dh_final is None else dh_final
-    dh0 = x.new_empty(per_seq, dtype=f32) if like is None else torch.empty_like(like)
+    dx, dh0 = torch.empty_like(x), states.new_empty(N, C)
     ws, wsp, nbytes = _workspace_of(lib().kda_gated_scan_workspace_size(T, C), ws, x,
                                     "kda_gated_scan_workspace_size")
     if z is None:
         dg = torch.empty_like(g)
-        _call(lib().kda_gated_scan_g_backward, dev, stream, xp, gp, *common, dx.data_ptr(),
+        _call(lib().kda_gated_scan_g_backward, dev, xp, gp, *common, dx.data_ptr(),
               dg.data_ptr(), dh0.data_ptr(), wsp, nbytes)
         return dx, dg, dh0
     dz, dA = torch.empty_like(z), torch.empty_like(A)
-    _call(lib().kda_gated_scan_backward, dev, stream, xp, zp, Ap, *common, dx.data_ptr(),
+    _call(lib().kda_gated_scan_backward, dev, xp, zp, Ap, *common, dx.data_ptr(),
           dz.data_ptr(), dA.data_ptr(), dh0.data_ptr(), wsp, nbytes)
     return dx, dz, dA, dh0
 
@@ -825,11 +839,14 @@ def gated_scan_g_backward(x, g, states, dy, *, h0=None, dh_final=None, cu_seqlen
 def gated_scan_step(x, z, A, h, *, y=None, stream=None):
     """One step of gated_scan for B sequences: x, z [B, ...], A [channels] fp32;
     h [B, channels] fp32 is updated in place.  Returns y (x's shape and dtype)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gated_scan_step(x, z, A, h, y=y)
     B, C, _, _ = _packed(x, None, 1, None)
     dev, dt, f32, shape = x.get_device(), x.dtype, torch.float32, x.shape
     if y is None:
         y = torch.empty_like(x)
-    _call(lib().kda_gated_scan_step, dev, stream, _role("x", x, shape, dt, dev),
+    _call(lib().kda_gated_scan_step, dev, _role("x", x, shape, dt, dev),
           _role("z", z, shape, dt, dev), _role("A", A, (C,), f32, dev),
           _role("h", h, (B, C), f32, dev), B, C, _dt(x), _role("y", y, shape, dt, dev))
     return y
@@ -875,13 +892,17 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     channels, paired (i, i + rot/2), or (2i, 2i+1) when ``interleaved``.  q and
     k may be slices of one projection's output (heads side by side, any token
     stride); q_out = q, k_out = k works in place.  Returns (q_out, k_out)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qk_norm_rope(q, k, positions, freqs, q_weight=q_weight, k_weight=k_weight,
+                                eps=eps, interleaved=interleaved, q_out=q_out, k_out=k_out)
     T, d, rot, read = _qk(q, k, positions, freqs, q_weight, k_weight)
     dev, dt, qs, ks = q.get_device(), q.dtype, q.shape, k.shape
     if q_out is None:
         q_out = _new_heads(q)
     if k_out is None:
         k_out = _new_heads(k)
-    _call(lib().kda_qk_norm_rope, dev, stream, *_head_rows("q", q, qs, dt, dev),
+    _call(lib().kda_qk_norm_rope, dev, *_head_rows("q", q, qs, dt, dev),
           *_head_rows("k", k, ks, dt, dev), *read, eps, T, qs[1], ks[1], d, rot,
           1 if interleaved else 0, _dt(q), *_head_rows("q_out", q_out, qs, dt, dev),
           *_head_rows("k_out", k_out, ks, dt, dev))
@@ -895,6 +916,12 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, positions, freqs, *, q_weight=No
     rest as given to it; dq = dq_out, dk = dk_out works in place.  Returns
     (dq, dk, dq_weight, dk_weight), the last two [d] fp32 or None where the
     gain is None."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qk_norm_rope_backward(q, k, dq_out, dk_out, positions, freqs,
+                                         q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                         interleaved=interleaved, dq=dq, dk=dk,
+                                         workspace=workspace)
     T, d, rot, read = _qk(q, k, positions, freqs, q_weight, k_weight)
     dev, dt, qs, ks = q.get_device(), q.dtype, q.shape, k.shape
     if dq is None:
@@ -905,7 +932,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, positions, freqs, *, q_weight=No
     dkw = None if k_weight is None else torch.empty_like(k_weight)
     ws, wsp, nbytes = _workspace_of(lib().kda_qk_norm_rope_backward_workspace_size(T, d),
                                     workspace, q, "kda_qk_norm_rope_backward_workspace_size")
-    _call(lib().kda_qk_norm_rope_backward, dev, stream, *_head_rows("q", q, qs, dt, dev),
+    _call(lib().kda_qk_norm_rope_backward, dev, *_head_rows("q", q, qs, dt, dev),
           *_head_rows("k", k, ks, dt, dev), *_head_rows("dq_out", dq_out, qs, dt, dev),
           *_head_rows("dk_out", dk_out, ks, dt, dev), *read, eps, T, qs[1], ks[1], d, rot,
           1 if interleaved else 0, _dt(q), *_head_rows("dq", dq, qs, dt, dev),

@@ -247,3 +247,80 @@ def test_empty_problem():
     assert torch.equal(dh0, h0) and (dA == 0).all()
     y, h = kda.gated_scan_g(x, x, cu_seqlens=cu, max_seqlen=0)
     assert (h == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_in_place_state_of_sequences_inside_one_span(dtype):
+    """A sequence's start and its end lie in one warp's span: h0 is read before
+    h_final, which is the same tensor, is written."""
+    p = make([10, 8, 20, 3, 1, 1, 30], 16, dtype, "z", seed=21)
+    out, _ = run(p)
+    h = cuda(p["h0"]).clone()
+    y, hf = kda.gated_scan(cuda(p["x"]), *gate_of(p), h0=h, h_final=h, cu_seqlens=cuda(p["cu"]),
+                           max_seqlen=30)
+    assert torch.equal(hf, out[1]) and torch.equal(y, out[0])
+
+
+def test_in_place_state_with_a_split_token_axis():
+    p = make([3000, 5, 2900], 16, "bf16", "z", seed=22)
+    f = scan.forward(p["x"], p["cu"].tolist(), z=p["z"], A=p["A"], h0=p["h0"])
+    h = cuda(p["h0"]).clone()
+    y, hf = kda.gated_scan(cuda(p["x"]), *gate_of(p), h0=h, h_final=h, cu_seqlens=cuda(p["cu"]),
+                           max_seqlen=3000)
+    close(hf, f["h_final"], f["e_h_final"], "h_final")
+    close(y, f["y"], f["e_y"], "y")
+
+
+@pytest.mark.parametrize("entry", ["z", "g"])
+def test_thousands_of_short_sequences(entry):
+    rng = np.random.default_rng(23)
+    p = make([int(v) for v in rng.integers(0, 4, 3000)], 16, "f32", entry, seed=23)
+    check(p, *run(p))
+
+
+@pytest.mark.parametrize("entry", ["z", "g"])
+def test_padded_batch_with_a_split_token_axis(entry):
+    """The last sequence ends inside a segment; the segments behind it have nothing to do."""
+    p = make([1500, 0, 700], 16, "bf16", entry, seed=24, pad=6000)
+    y = torch.full_like(cuda(p["x"]), 7.0)
+    out, grads = run(p, y=y)
+    assert (y[2200:] == 7).all()
+    check(p, out, grads)
+
+
+def test_no_sequence_has_tokens():
+    p = make([0, 0], 16, "bf16", "z", seed=25, pad=100) | dict(L=0)
+    out, grads = run(p)
+    assert torch.equal(out[1].cpu(), p["h0"]) and torch.equal(grads[3].cpu(), p["dh"])
+    assert (grads[2] == 0).all()
+
+
+def test_workspace_contents_do_not_matter():
+    p = make([4000, 30, 2000], 24, "bf16", "z", seed=26)
+    want, want_grads = run(p)
+    n = kda.kda_gated_scan_workspace_size(p["T"], 24)
+    how = dict(cu_seqlens=cuda(p["cu"]), max_seqlen=4000, h0=cuda(p["h0"]))
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    out = kda.gated_scan(cuda(p["x"]), *gate_of(p), save_states=True, workspace=ws, **how)
+    ws.fill_(255)
+    grads = kda.gated_scan_backward(cuda(p["x"]), *gate_of(p), out[2], cuda(p["dy"]),
+                                    dh_final=cuda(p["dh"]), workspace=ws, **how)
+    for a, b in zip((*out[:2], *grads), (*want[:2], *want_grads)):
+        assert torch.equal(a, b)
+
+
+def test_stream_argument():
+    p = make([4000, 200], 24, "bf16", "z", seed=27)
+    want, want_grads = run(p)
+    x, gate, h0, dy, dh = (cuda(p["x"]), gate_of(p), cuda(p["h0"]), cuda(p["dy"]), cuda(p["dh"]))
+    how = dict(cu_seqlens=cuda(p["cu"]), max_seqlen=4000, h0=h0)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    out = kda.gated_scan(x, *gate, save_states=True, stream=side, **how)
+    grads = kda.gated_scan_backward(x, *gate, out[2], dy, dh_final=dh, stream=side, **how)
+    # a workspace of the calls that was handed out again here would be overwritten now
+    junk = [torch.full((1 << 16,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    for a, b in zip((*out[:2], *grads), (*want[:2], *want_grads)):
+        assert torch.equal(a, b)
+    del junk

@@ -142,6 +142,23 @@ def test_gated_scan_rejects_missing_gradient_arguments():
     assert _scan("z", N=0, T=0, L=0, x=None, gate=None, A=None, out=None) == kda.KDA_OK
 
 
+def test_sizes_beyond_the_kernels_arithmetic_are_refused():
+    T = 0x7fffff01
+    assert _scan("z", T=T, L=T) == UNS and _scan("g", True, T=T, L=T) == UNS
+    assert kda.kda_short_conv_swish_backward(FAKE, FAKE, FAKE, None, 1, T, T, 8, 4, kda.KDA_BF16,
+                                             FAKE, FAKE, FAKE, 1 << 60, None) == UNS
+    # (Hq + Hk) * d above 2^20
+    assert kda.kda_qk_norm_rope(FAKE, 1 << 20, FAKE, 64, FAKE, FAKE, None, None, 1e-6, 1,
+                                1 << 14, 1, 64, 64, 0, kda.KDA_BF16, FAKE, 1 << 20, FAKE, 64,
+                                None) == UNS
+
+
+def test_gradient_of_the_initial_state_is_not_written_over_the_final_states():
+    st = kda.kda_gated_scan_g_backward(FAKE, FAKE, FAKE, None, None, 1, 64, 64, 32, kda.KDA_F32,
+                                       FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 40, None)
+    assert st == BAD
+
+
 def test_gated_scan_step_rejects_bad_arguments():
     def step(x=FAKE, h=FAKE, B=4, C=32, dt=kda.KDA_F32):
         return kda.kda_gated_scan_step(x, FAKE, FAKE, h, B, C, dt, FAKE, None)
