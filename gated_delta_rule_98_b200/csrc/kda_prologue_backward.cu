@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(256)
 // computed twice) that still gives every SM four blocks, else the shortest.
 void split(int T, int channels, int& run, int& splits) {
   const int64_t cols = (channels + kCols - 1) / kCols;
-  run = 64;
+  run = 128;
   int64_t tiles;
   for (;; run /= 2) {
     tiles = ((int64_t)T + kWarps * run - 1) / (kWarps * run);
