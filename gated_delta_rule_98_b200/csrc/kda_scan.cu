@@ -78,19 +78,20 @@ __device__ __forceinline__ void stg2(__nv_bfloat16* p, float2 v) {
 __device__ __forceinline__ void stg2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
 
 // a = 2^t and 1 - a, t = g log2(e) <= 0.  Near 1 the difference loses digits, so
-// above 2^-0.36 = 0.78 it is t times a polynomial: (1 - 2^t) / t interpolated at
-// the Chebyshev nodes of [-0.3605, 0] (a few units of 2^-24 there).
+// above 2^-0.2 = 0.87 it is t times a polynomial: (1 - 2^t) / t interpolated at
+// the Chebyshev nodes of [-0.2005, 0] (5e-8 of it at most); below, the rounding of
+// a is at most 15 units of 2^-24 of 1 - a.
 __device__ __forceinline__ void decay(float2 t, float2& a, float2& m) {
   a = make_float2(ex2(t.x), ex2(t.y));
-  float2 q = splat(-0.00120225688f);
-  q = __ffma2_rn(q, t, splat(-0.00957753696f));
-  q = __ffma2_rn(q, t, splat(-0.0554989241f));
-  q = __ffma2_rn(q, t, splat(-0.240226269f));
+  float2 q = splat(-0.00910008978f);
+  q = __ffma2_rn(q, t, splat(-0.0554398298f));
+  q = __ffma2_rn(q, t, splat(-0.240223944f));
   q = __ffma2_rn(q, t, splat(-0.693147182f));
   q = __fmul2_rn(q, t);
-  m = __ffma2_rn(a, splat(-1.f), splat(1.f));
-  m.x = t.x > -0.36f ? q.x : m.x;
-  m.y = t.y > -0.36f ? q.y : m.y;
+  // single additions here and in the sigmoid take their constant from the
+  // instruction, a packed one from two registers, which are scarce
+  m.x = t.x > -0.2f ? q.x : 1.f - a.x;
+  m.y = t.y > -0.2f ? q.y : 1.f - a.y;
 }
 
 // The library's gate on two channels: k = -e^A log2(e).
@@ -101,7 +102,7 @@ template <bool kSlope>
 __device__ __forceinline__ GateZ gate_z(float2 z, float2 k) {
   const float2 u = __fmul2_rn(z, k);
   const float2 e = make_float2(ex2(u.x), ex2(u.y));  // e^{-e^A z}
-  const float2 d = __fadd2_rn(e, splat(1.f));
+  const float2 d = make_float2(e.x + 1.f, e.y + 1.f);
   const float2 s = make_float2(rcp(d.x), rcp(d.y));
   GateZ g;
   decay(__fmul2_rn(s, splat(kGateMin * kLog2e)), g.a, g.m);
@@ -762,10 +763,13 @@ __global__ void __launch_bounds__(256)
 
 // ----------------------------------------------------------------- launch ----
 
-// Segments of the token axis: two blocks per SM at least when the channels
-// alone give few, segments of 1024 tokens at least.
+// Segments of the token axis.  None where the channels alone give a block to half
+// the SMs: the maps' launch costs more than the idle SMs (32768 x 1408 bf16: 103 us
+// in one segment, 127 in three; 32768 x 1024: 103 and 100, its gradient 168 and
+// 143).  Below, two blocks per SM (32768 x 512: 53 us with 296 blocks, 67 with 148,
+// 63 with 444), segments of 1024 tokens at least.
 int segments(int T, int cols) {
-  if (cols >= 100) return 1;
+  if (cols >= 74) return 1;
   const int s = 296 / cols < T / 1024 ? 296 / cols : T / 1024;
   return s < 1 ? 1 : s > kMaxSegments ? kMaxSegments : s;
 }
