@@ -270,22 +270,23 @@ __global__ void __launch_bounds__(256)
 }
 
 // Tokens of a run and blocks along the tokens: the longest run (fewest tokens
-// computed twice) that still gives every SM four blocks, else the shortest.
-void split(int T, int channels, int& run, int& splits) {
+// computed twice, fewest weight sums) that gives `want` blocks, else the shortest.
+void split(int T, int channels, int want, int& run, int& splits) {
   const int64_t cols = (channels + kCols - 1) / kCols;
   run = 128;
   int64_t tiles;
   for (;; run /= 2) {
     tiles = ((int64_t)T + kWarps * run - 1) / (kWarps * run);
-    if (run == kGroup || tiles * cols >= 4 * 148) break;
+    if (run == kGroup || tiles * cols >= want) break;
   }
   splits = (int)(tiles < 1 ? 1 : tiles > kMaxSplits ? kMaxSplits : tiles);
 }
+int blocks_wanted(bool bf16) { return bf16 ? 240 : 120; }
 
 template <typename T, int W>
 cudaError_t launch_w(const ConvBackwardArgs& a) {
   int run, splits;
-  split(a.T, a.channels, run, splits);
+  split(a.T, a.channels, blocks_wanted(a.bf16), run, splits);
   constexpr int smem = kWarps * kSlots * 2 * kGroup * kCols * (int)sizeof(T);
   static_assert(smem >= kWarps * W * kCols * (int)sizeof(float), "dw fits the slots");
   auto* kernel = conv_swish_backward_kernel<T, W>;
@@ -317,7 +318,7 @@ cudaError_t launch_t(const ConvBackwardArgs& a) {
 
 size_t conv_backward_workspace_bytes(int T, int channels, int width) {
   int run, splits;
-  split(T, channels, run, splits);
+  split(T, channels, blocks_wanted(true), run, splits);  // of the two types' the more
   return (size_t)splits * channels * width * sizeof(float);
 }
 
