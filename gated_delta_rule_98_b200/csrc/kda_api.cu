@@ -7,6 +7,7 @@
 #include "../../include/kda.h"
 #include "kda_common.cuh"
 #include "kda_launch.h"
+#include "kda_layer.h"
 
 namespace {
 

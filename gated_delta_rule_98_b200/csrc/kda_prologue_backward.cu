@@ -15,7 +15,7 @@
 // take 8 runs that follow one another and add their dw through shared memory;
 // the blocks' sums are added by a second launch, in a fixed order.
 #include "kda_common.cuh"
-#include "kda_launch.h"
+#include "kda_layer.h"
 
 namespace kda {
 

@@ -16,7 +16,7 @@
 // are fixed while it does and a row costs few instructions besides its
 // arithmetic; the many resident blocks hide the rest.
 #include "kda_common.cuh"
-#include "kda_launch.h"
+#include "kda_layer.h"
 
 namespace kda {
 

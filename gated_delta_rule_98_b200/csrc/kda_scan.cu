@@ -37,7 +37,7 @@
 
 #include "../../include/kda.h"
 #include "kda_common.cuh"
-#include "kda_launch.h"
+#include "kda_layer.h"
 
 namespace kda {
 
