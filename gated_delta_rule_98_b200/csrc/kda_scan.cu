@@ -44,10 +44,13 @@ namespace kda {
 namespace {
 
 constexpr int kSaved = KDA_SCAN_INTERVAL;  // tokens between saved states
-// Warps of a block that has an SM to itself (half as many where two share one): at
-// most 15 (a named barrier each, 0 is __syncthreads), and what the registers allow.
-constexpr int kWarps = 15;      // forward: 128 registers a thread
-constexpr int kWarpsBack = 12;  // gradient: 168
+// Warps of a block that has an SM to itself, and of one of two that share an SM: at
+// most 15 (a named barrier each, 0 is __syncthreads), and what the registers allow:
+// 128 a thread in the forward (96 are slower, 203 -> 293 us at 65536 x 2048); in the
+// gradient 168 alone (65536 x 2048: 340 us, with 128: 361) and 128 in pairs (32768 x
+// 4096: 336 us, with 168 and 6 warps 356).
+constexpr int kAlone = 15, kPaired = 8;
+constexpr int kAloneBack = 12, kPairedBack = 8;
 constexpr int kSlots = 3;     // spans of a warp in flight or in use
 constexpr int kMaxSegments = 64;
 constexpr int kRoom = 222 * 1024;  // dynamic shared memory of a block that has an SM to itself
@@ -328,7 +331,7 @@ __device__ __forceinline__ void pass_empty(const Bounds& b, const float* from, f
 // kMaps: form the segment's map (P, H) in `maps` instead of y; else compose
 // the maps of the segments before this one.
 template <typename T, bool kZ, bool kMaps, int SPAN>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__(kAlone * 32, 1)
     scan_kernel(const ScanArgs a, int seg_spans, float* maps) {
   using G = Geo<T, SPAN>;
   using E = typename std::conditional<kZ, T, float>::type;
@@ -494,15 +497,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 // kMaps: form the map of the gradient through the segment, from its last token
 // to its first, in `maps`; else compose the maps of the segments after this
 // one.  dA of the segment's tokens goes to row blockIdx.y of dA_part.
-template <typename T, bool kZ, bool kMaps, int SPAN>
-__global__ void __launch_bounds__(kWarpsBack * 32, 1)
+template <typename T, bool kZ, bool kMaps, int SPAN, bool kPair>
+__global__ void __launch_bounds__((kPair ? kPairedBack : kAloneBack) * 32, kPair ? 2 : 1)
     scan_backward_kernel(const ScanArgs a, int seg_spans, float* maps, float* dA_part) {
   using G = Geo<T, SPAN>;
   using E = typename std::conditional<kZ, T, float>::type;
   constexpr int XB = tile_bytes<G, T>(), ZB = tile_bytes<G, E>(), STAGE = 2 * XB + ZB, D = kSlots;
   constexpr int K = G::K, LC = G::LC, CB = G::CB;
   extern __shared__ __align__(16) unsigned char s_raw[];
-  __shared__ float2 s_h[2][LC], s_p[2][LC], s_dA[kWarpsBack][LC];
+  __shared__ float2 s_h[2][LC], s_p[2][LC], s_dA[kPair ? kPairedBack : kAloneBack][LC];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
   const int l = lane % LC, grp = lane / LC;
   const int C = a.C, c0 = blockIdx.x * CB, c = c0 + 2 * l;
@@ -776,11 +779,10 @@ int segments(int T, int cols) {
 
 struct Plan {
   int cols, segs, seg_spans, warps, smem;
+  bool pair;  // two blocks an SM: when there are more blocks than SMs
 };
-// Warps and shared memory: one block of up to most_warps warps on an SM, or two
-// of half as many when there are more blocks than SMs.
 template <typename G>
-Plan plan(const ScanArgs& a, int warp_bytes, int most_warps, bool one_segment) {
+Plan plan(const ScanArgs& a, int warp_bytes, int alone, int paired, bool one_segment) {
   constexpr int SPAN = G::GR * G::K;
   Plan p;
   p.cols = (a.C + G::CB - 1) / G::CB;
@@ -788,8 +790,8 @@ Plan plan(const ScanArgs& a, int warp_bytes, int most_warps, bool one_segment) {
   const int segs = one_segment ? 1 : segments(a.T, p.cols);
   p.seg_spans = spans > 0 ? (spans + segs - 1) / segs : 1;
   p.segs = spans > 0 ? (spans + p.seg_spans - 1) / p.seg_spans : 1;
-  const bool two = (int64_t)p.cols * p.segs > 148;
-  const int room = two ? kRoom / 2 - 1024 : kRoom, most = two ? (most_warps + 1) / 2 : most_warps;
+  p.pair = (int64_t)p.cols * p.segs > 148;
+  const int room = p.pair ? kRoom / 2 - 1024 : kRoom, most = p.pair ? paired : alone;
   p.warps = room / warp_bytes < most ? room / warp_bytes : most;
   if (p.warps > p.seg_spans) p.warps = p.seg_spans;
   p.smem = p.warps * warp_bytes;
@@ -808,7 +810,7 @@ cudaError_t forward_t(const ScanArgs& a) {
   using G = Geo<T, SPAN>;
   using E = typename std::conditional<kZ, T, float>::type;
   // a later segment writes h_final while an earlier one reads h0: not in place
-  const Plan p = plan<G>(a, kSlots * (tile_bytes<G, T>() + tile_bytes<G, E>()), kWarps,
+  const Plan p = plan<G>(a, kSlots * (tile_bytes<G, T>() + tile_bytes<G, E>()), kAlone, kPaired,
                          a.h0 && a.h0 == a.h_final);
   float* maps = (float*)a.ws;
   const dim3 grid(p.cols, p.segs);
@@ -825,21 +827,16 @@ cudaError_t forward_t(const ScanArgs& a) {
   return cudaGetLastError();
 }
 
-template <typename T, bool kZ>
-cudaError_t backward_t(const ScanArgs& a) {
-  constexpr int SPAN = sizeof(T) == 2 ? 32 : 64;  // 8 tokens a run
-  using G = Geo<T, SPAN>;
-  using E = typename std::conditional<kZ, T, float>::type;
-  const Plan p =
-      plan<G>(a, kSlots * (2 * tile_bytes<G, T>() + tile_bytes<G, E>()), kWarpsBack, false);
+template <typename T, bool kZ, int SPAN, bool kPair>
+cudaError_t backward_p(const ScanArgs& a, const Plan& p) {
   float* maps = (float*)a.ws;
   float* part = p.segs > 1 ? maps + (size_t)2 * p.segs * a.C : a.dA;
   const dim3 grid(p.cols, p.segs);
-  auto* run = scan_backward_kernel<T, kZ, false, SPAN>;
+  auto* run = scan_backward_kernel<T, kZ, false, SPAN, kPair>;
   cudaError_t err = allow(run);
   if (err != cudaSuccess) return err;
   if (p.segs > 1) {
-    auto* form = scan_backward_kernel<T, kZ, true, SPAN>;
+    auto* form = scan_backward_kernel<T, kZ, true, SPAN, kPair>;
     if ((err = allow(form)) != cudaSuccess) return err;
     form<<<grid, p.warps * 32, p.smem, a.stream>>>(a, p.seg_spans, maps, nullptr);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
@@ -848,6 +845,16 @@ cudaError_t backward_t(const ScanArgs& a) {
   if ((err = cudaGetLastError()) != cudaSuccess || !kZ || p.segs == 1) return err;
   sum_rows_kernel<<<(a.C + 63) / 64, 64, 0, a.stream>>>(part, p.segs, a.C, a.dA);
   return cudaGetLastError();
+}
+
+template <typename T, bool kZ>
+cudaError_t backward_t(const ScanArgs& a) {
+  constexpr int SPAN = sizeof(T) == 2 ? 32 : 64;  // 8 tokens a run
+  using G = Geo<T, SPAN>;
+  using E = typename std::conditional<kZ, T, float>::type;
+  const Plan p = plan<G>(a, kSlots * (2 * tile_bytes<G, T>() + tile_bytes<G, E>()), kAloneBack,
+                         kPairedBack, false);
+  return p.pair ? backward_p<T, kZ, SPAN, true>(a, p) : backward_p<T, kZ, SPAN, false>(a, p);
 }
 
 }  // namespace
