@@ -670,6 +670,13 @@ def _role(name, t, shape, dtype, device):
                      f"{tuple(shape)} {dtype} on the GPU of the first tensor")
 
 
+def _first(name, t):
+    """Address of the tensor that the others are held to."""
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -721,18 +728,22 @@ def short_conv_swish_backward(x, w, dy, *, cu_seqlens=None, num_seqs=None, max_s
     T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
     width = w.shape[-1]
     dev, dt, f32, shape, taps = x.get_device(), x.dtype, torch.float32, x.shape, (C, width)
-    xp, wp = _role("x", x, shape, dt, dev), _role("w", w, taps, f32, dev)
+    xp, wp = _first("x", x), _role("w", w, taps, f32, dev)
     dyp = _role("dy", dy, shape, dt, dev)
     cup = _role("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
     if dx is None:
         dx = torch.empty_like(x)
+    else:
+        _role("dx", dx, shape, dt, dev)
     if dw is None:
         dw = torch.empty_like(w)
+    else:
+        _role("dw", dw, taps, f32, dev)
     ws, wsp, nbytes = _workspace_of(
         lib().kda_short_conv_swish_backward_workspace_size(T, C, width), workspace, x,
         "kda_short_conv_swish_backward_workspace_size")
     _call(lib().kda_short_conv_swish_backward, dev, xp, wp, dyp, cup, N, T, L, C, width,
-          _dt(x), _role("dx", dx, shape, dt, dev), _role("dw", dw, taps, f32, dev), wsp, nbytes)
+          _dt(x), dx.data_ptr(), dw.data_ptr(), wsp, nbytes)
     return dx, dw
 
 
@@ -745,24 +756,31 @@ def _gated_scan(x, z, A, g, h0, cu_seqlens, num_seqs, max_seqlen, y, h_final, st
     T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
     dev, dt, f32, shape, per_seq = x.get_device(), x.dtype, torch.float32, x.shape, (N, C)
     rows = ((T + KDA_SCAN_INTERVAL - 1) // KDA_SCAN_INTERVAL, C)
-    xp, h0p = _role("x", x, shape, dt, dev), _role("h0", h0, per_seq, f32, dev)
+    xp, h0p = _first("x", x), _role("h0", h0, per_seq, f32, dev)
     cup = _role("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
     if z is None:
         fn, gate = lib().kda_gated_scan_g, (_role("g", g, shape, f32, dev),)
     else:
         fn = lib().kda_gated_scan
         gate = (_role("z", z, shape, dt, dev), _role("A", A, (C,), f32, dev))
+    like = A if g is None else g
     if y is None:
         y = torch.empty_like(x)
+    else:
+        _role("y", y, shape, dt, dev)
     if h_final is None:
-        h_final = (A if g is None else g).new_empty(N, C)
-    if states is None and save_states:
-        states = (A if g is None else g).new_empty(*rows)
+        h_final = like.new_empty(N, C)
+    else:
+        _role("h_final", h_final, per_seq, f32, dev)
+    if states is not None:
+        _role("states", states, rows, f32, dev)
+    elif save_states:
+        states = like.new_empty(*rows)
     ws, wsp, nbytes = _workspace_of(lib().kda_gated_scan_workspace_size(T, C), ws, x,
                                     "kda_gated_scan_workspace_size")
     _call(fn, dev, xp, *gate, h0p, cup, N, T, L, C, _dt(x),
-          _role("y", y, shape, dt, dev), _role("h_final", h_final, per_seq, f32, dev),
-          _role("states", states, rows, f32, dev), wsp, nbytes)
+          y.data_ptr(),
+          h_final.data_ptr(), None if states is None else states.data_ptr(), wsp, nbytes)
     return (y, h_final) if states is None else (y, h_final, states)
 
 
@@ -798,7 +816,7 @@ def _gated_scan_backward(x, z, A, g, states, dy, h0, dh_final, cu_seqlens, num_s
     T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
     dev, dt, f32, shape, per_seq = x.get_device(), x.dtype, torch.float32, x.shape, (N, C)
     rows = ((T + KDA_SCAN_INTERVAL - 1) // KDA_SCAN_INTERVAL, C)
-    xp = _role("x", x, shape, dt, dev)
+    xp = _first("x", x)
     common = (_role("states", states, rows, f32, dev), _role("h0", h0, per_seq, f32, dev),
               _role("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev), N, T, L, C, _dt(x),
               _role("dy", dy, shape, dt, dev), _role("dh_final", dh_final, per_seq, f32, dev))
@@ -846,9 +864,11 @@ def gated_scan_step(x, z, A, h, *, y=None, stream=None):
     dev, dt, f32, shape = x.get_device(), x.dtype, torch.float32, x.shape
     if y is None:
         y = torch.empty_like(x)
-    _call(lib().kda_gated_scan_step, dev, _role("x", x, shape, dt, dev),
+    else:
+        _role("y", y, shape, dt, dev)
+    _call(lib().kda_gated_scan_step, dev, _first("x", x),
           _role("z", z, shape, dt, dev), _role("A", A, (C,), f32, dev),
-          _role("h", h, (B, C), f32, dev), B, C, _dt(x), _role("y", y, shape, dt, dev))
+          _role("h", h, (B, C), f32, dev), B, C, _dt(x), y.data_ptr())
     return y
 
 
@@ -900,12 +920,17 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     dev, dt, qs, ks = q.get_device(), q.dtype, q.shape, k.shape
     if q_out is None:
         q_out = _new_heads(q)
+        qo = q_out.data_ptr(), qs[1] * d
+    else:
+        qo = _head_rows("q_out", q_out, qs, dt, dev)
     if k_out is None:
         k_out = _new_heads(k)
+        ko = k_out.data_ptr(), ks[1] * d
+    else:
+        ko = _head_rows("k_out", k_out, ks, dt, dev)
     _call(lib().kda_qk_norm_rope, dev, *_head_rows("q", q, qs, dt, dev),
           *_head_rows("k", k, ks, dt, dev), *read, eps, T, qs[1], ks[1], d, rot,
-          1 if interleaved else 0, _dt(q), *_head_rows("q_out", q_out, qs, dt, dev),
-          *_head_rows("k_out", k_out, ks, dt, dev))
+          1 if interleaved else 0, _dt(q), *qo, *ko)
     return q_out, k_out
 
 
@@ -926,8 +951,14 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, positions, freqs, *, q_weight=No
     dev, dt, qs, ks = q.get_device(), q.dtype, q.shape, k.shape
     if dq is None:
         dq = _new_heads(q)
+        qo = dq.data_ptr(), qs[1] * d
+    else:
+        qo = _head_rows("dq", dq, qs, dt, dev)
     if dk is None:
         dk = _new_heads(k)
+        ko = dk.data_ptr(), ks[1] * d
+    else:
+        ko = _head_rows("dk", dk, ks, dt, dev)
     dqw = None if q_weight is None else torch.empty_like(q_weight)
     dkw = None if k_weight is None else torch.empty_like(k_weight)
     ws, wsp, nbytes = _workspace_of(lib().kda_qk_norm_rope_backward_workspace_size(T, d),
@@ -935,8 +966,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, positions, freqs, *, q_weight=No
     _call(lib().kda_qk_norm_rope_backward, dev, *_head_rows("q", q, qs, dt, dev),
           *_head_rows("k", k, ks, dt, dev), *_head_rows("dq_out", dq_out, qs, dt, dev),
           *_head_rows("dk_out", dk_out, ks, dt, dev), *read, eps, T, qs[1], ks[1], d, rot,
-          1 if interleaved else 0, _dt(q), *_head_rows("dq", dq, qs, dt, dev),
-          *_head_rows("dk", dk, ks, dt, dev), None if dqw is None else dqw.data_ptr(),
+          1 if interleaved else 0, _dt(q), *qo, *ko, None if dqw is None else dqw.data_ptr(),
           None if dkw is None else dkw.data_ptr(), wsp, nbytes)
     return dq, dk, dqw, dkw
 
