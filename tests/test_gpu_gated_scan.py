@@ -324,3 +324,22 @@ def test_stream_argument():
     for a, b in zip((*out[:2], *grads), (*want[:2], *want_grads)):
         assert torch.equal(a, b)
     del junk
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements: the last sequence, alone, gives the same bits."""
+    T, C, tail = 65600, 32768, 96          # the tail starts on a span
+    x, z, dy = (torch.zeros(T, C, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    for i, t in enumerate((x, z, dy)):
+        t[-tail:] = draw(30 + i, "bf16", tail, C, mean=-3.0 if t is z else 0.0).cuda()
+    A = draw(33, "f32", C, std=0.3).cuda()
+    cu = torch.tensor([0, T - tail, T], dtype=torch.int32, device="cuda")
+    how = dict(cu_seqlens=cu, max_seqlen=T)
+    y, h, st = kda.gated_scan(x, z, A, save_states=True, **how)
+    dx, dz, _, dh0 = kda.gated_scan_backward(x, z, A, st, dy, **how)
+    a, b, c = (t[-tail:].clone() for t in (x, z, dy))
+    y1, h1, st1 = kda.gated_scan(a, b, A, save_states=True)
+    dx1, dz1, _, dh1 = kda.gated_scan_backward(a, b, A, st1, c)
+    assert torch.equal(y[-tail:], y1) and torch.equal(h[1:], h1)
+    assert torch.equal(dx[-tail:], dx1) and torch.equal(dz[-tail:], dz1)
+    assert torch.equal(dh0[1:], dh1) and (y[:100] == 0).all() and (y[-tail - 9:-tail] == 0).all()

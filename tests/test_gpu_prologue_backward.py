@@ -125,3 +125,17 @@ def test_trains_the_recurrent_block():
     o = scan.conv_backward(p["x"], p["w"], cu, du.cpu())
     close(dx, o["dx"], o["e_dx"], "dx")
     close(dw, o["dw"], o["e_dw"], "dw")
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements: the last sequence, alone, gives the same bits."""
+    T, C, tail = 65600, 32768, 96
+    x, dy = (torch.zeros(T, C, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[-tail:], dy[-tail:] = draw(40, "bf16", tail, C).cuda(), draw(41, "bf16", tail, C).cuda()
+    w = draw(42, "f32", C, 4, std=0.5).cuda()
+    cu = torch.tensor([0, T - tail, T], dtype=torch.int32, device="cuda")
+    dx, dw = kda.short_conv_swish_backward(x, w, dy, cu_seqlens=cu, max_seqlen=T)
+    dx1, dw1 = kda.short_conv_swish_backward(x[-tail:].clone(), w, dy[-tail:].clone())
+    assert torch.equal(dx[-tail:], dx1) and (dx[:100] == 0).all()
+    # dw's sums are grouped otherwise: tail terms of magnitude |du x|, each rounded
+    assert ((dw - dw1).abs() <= tail * 2.0 ** -24 * 30).all()

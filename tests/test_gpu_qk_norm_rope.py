@@ -173,3 +173,36 @@ def test_rotated_queries_and_keys_through_the_operator():
     o_ref, S_ref = ref.forward(q.cpu(), k.cpu(), inp["v"], inp["beta"], z=inp["z"], A=inp["A"])
     assert_close(o, o_ref, torch.bfloat16, "o")
     assert_close(S, S_ref, torch.bfloat16, "S_final")
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements: the last tokens, alone, give the same bits."""
+    T, H, d, tail = 65600, 256, 128, 40
+    q, dq = (torch.zeros(T, H, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q[-tail:], dq[-tail:] = draw(50, "bf16", tail, H, d).cuda(), draw(51, "bf16", tail, H, d).cuda()
+    k = torch.ones(T, 1, d, dtype=torch.bfloat16, device="cuda")
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    freqs = torch.from_numpy(10000.0 ** (-2.0 * np.arange(d // 2) / d)).cuda()
+    out = kda.qk_norm_rope(q, k, pos, freqs)
+    back = kda.qk_norm_rope_backward(q, k, dq, k, pos, freqs)
+    cut = lambda t: t[-tail:].clone()
+    out1 = kda.qk_norm_rope(cut(q), cut(k), cut(pos), freqs)
+    back1 = kda.qk_norm_rope_backward(cut(q), cut(k), cut(dq), cut(k), cut(pos), freqs)
+    assert torch.equal(out[0][-tail:], out1[0]) and torch.equal(back[0][-tail:], back1[0])
+    assert torch.equal(out[1][-tail:], out1[1]) and (out[0][:50] == 0).all()
+
+
+def test_stream_argument():
+    p = make(300, 4, 2, 64, 64, "bf16", seed=12)
+    want, want_back = call(p)
+    g = {k: cuda(v) for k, v in p.items()}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    how = dict(q_weight=g["qw"], k_weight=g["kw"], stream=side)
+    out = kda.qk_norm_rope(g["q"], g["k"], g["pos"], g["freqs"], **how)
+    back = kda.qk_norm_rope_backward(g["q"], g["k"], g["dq"], g["dk"], g["pos"], g["freqs"], **how)
+    junk = [torch.full((1 << 21,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    for a, b in zip((*out, *back), (*want, *want_back)):
+        assert torch.equal(a, b)
+    del junk
