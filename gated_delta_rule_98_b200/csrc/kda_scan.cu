@@ -53,6 +53,7 @@ constexpr int kAlone = 15, kPaired = 8;
 constexpr int kAloneBack = 12, kPairedBack = 8;
 constexpr int kSlots = 3;     // spans of a warp in flight or in use
 constexpr int kMaxSegments = 64;
+constexpr int kBrought = 256;  // states brought to the first cache: 16 KB
 constexpr int kRoom = 222 * 1024;  // dynamic shared memory of a block that has an SM to itself
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -316,6 +317,14 @@ __device__ __forceinline__ void put2(float* p, int n, int C, int c, bool in, flo
   if (p && in) *reinterpret_cast<float2*>(p + (size_t)n * C + c) = v;
 }
 
+// Brings the block's channels of the sequences' states near: a span with a sequence
+// start waits for them, and all spans behind it wait for that one.
+__device__ __forceinline__ void bring(const Bounds& b, const float* p, int C, int c0) {
+  if (!p) return;
+  for (int n = threadIdx.x; n < min(b.N, kBrought); n += blockDim.x)
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(p + (size_t)n * C + c0));
+}
+
 // What empty sequences hand through (`from`, or zeros) to `to`, for the block's channels.
 __device__ __forceinline__ void pass_empty(const Bounds& b, const float* from, float* to, int C,
                                            int c0, int CB) {
@@ -366,6 +375,7 @@ __global__ void __launch_bounds__(kAlone * 32, 1)
   const uint32_t tiles =
       (uint32_t)__cvta_generic_to_shared(s_raw) + warp * (D * STAGE);
   const unsigned char* tiles_p = s_raw + warp * (D * STAGE);
+  bring(b, a.h0, C, c0);
   const Source<G, T> X(a.x, C, c0, lane);
   const Source<G, E> Z(kZ ? a.z : (const void*)a.g, C, c0, lane);
   auto request = [&](int j, int slot) {
@@ -535,6 +545,8 @@ __global__ void __launch_bounds__((kPair ? kPairedBack : kAloneBack) * 32, kPair
   }
   const uint32_t tiles = (uint32_t)__cvta_generic_to_shared(s_raw) + warp * (D * STAGE);
   const unsigned char* tiles_p = s_raw + warp * (D * STAGE);
+  bring(b, a.h0, C, c0);
+  bring(b, a.dh_final, C, c0);
   const Source<G, T> X(a.x, C, c0, lane), DY(a.dy, C, c0, lane);
   const Source<G, E> Z(kZ ? a.z : (const void*)a.g, C, c0, lane);
   auto request = [&](int j, int slot) {
