@@ -782,10 +782,11 @@ __global__ void __launch_bounds__(256)
 // the SMs: the maps' launch costs more than the idle SMs (32768 x 1408 bf16: 103 us
 // in one segment, 127 in three; 32768 x 1024: 103 and 100, its gradient 168 and
 // 143).  Below, two blocks per SM (32768 x 512: 53 us with 296 blocks, 67 with 148,
-// 63 with 444), segments of 1024 tokens at least.
+// 63 with 444), segments of 512 tokens at least (4096 x 256: 14.7 us, with 1024
+// 17.9; 256 gains 2 us more there and costs short calls a launch).
 int segments(int T, int cols) {
   if (cols >= 74) return 1;
-  const int s = 296 / cols < T / 1024 ? 296 / cols : T / 1024;
+  const int s = 296 / cols < T / 512 ? 296 / cols : T / 512;
   return s < 1 ? 1 : s > kMaxSegments ? kMaxSegments : s;
 }
 
