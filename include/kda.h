@@ -381,7 +381,8 @@ kda_status kda_short_conv_swish(const void* x, const float* w, const int32_t* cu
  *  workspace : kda_short_conv_swish_backward_workspace_size bytes, 16-byte
  *              aligned, as in kda_forward.
  * u is recomputed from x.  Sums are float32 in a fixed order (bit-identical
- * from call to call).  Two launches.
+ * from call to call).  total_tokens at most 2^31 - 256 (else
+ * KDA_ERR_UNSUPPORTED).  One or two launches.
  */
 size_t kda_short_conv_swish_backward_workspace_size(int32_t total_tokens, int32_t channels,
                                                     int32_t width);
@@ -406,8 +407,9 @@ kda_status kda_short_conv_swish_backward(const void* x, const float* w, const vo
  *  x, z, y  : [T, channels] in `dt`; y must not overlap any input.
  *  A        : [channels] float32, per-channel gate scale (exp(A) is used).
  *  h0       : [N, channels] float32 or NULL (zeros).
- *  h_final  : [N, channels] float32 or NULL (not wanted); may equal h0.  An
- *             empty sequence passes h0 through.
+ *  h_final  : [N, channels] float32 or NULL (not wanted); may equal h0 (the
+ *             call then does not split the token axis over blocks, which is
+ *             slower with few channels).  An empty sequence passes h0 through.
  *  states   : [ceil(T / KDA_SCAN_INTERVAL), channels] float32 or NULL: row j
  *             receives the state entering packed token KDA_SCAN_INTERVAL * j
  *             (unspecified where that token starts a sequence).  The backward
@@ -417,11 +419,13 @@ kda_status kda_short_conv_swish_backward(const void* x, const float* w, const vo
  *             undefined values, never an out-of-range access) and
  *             cu_seqlens[N] may lie below total_tokens (a padded batch): rows
  *             from there on are not read, and y keeps what it held there.
- *  channels : a positive multiple of 8 (else KDA_ERR_UNSUPPORTED).
+ *  channels : a positive multiple of 8, at most 2^28; total_tokens at most
+ *             2^31 - 256 (else KDA_ERR_UNSUPPORTED).
  *  workspace: kda_gated_scan_workspace_size bytes, 16-byte aligned, as in
  *             kda_forward.
  * The state, the products of a and every sum are float32 in a fixed order
- * (bit-identical from call to call).
+ * (bit-identical from call to call).  One launch, two when few channels make
+ * it split the token axis; the gradients one to three.
  */
 #define KDA_SCAN_INTERVAL 32
 size_t kda_gated_scan_workspace_size(int32_t total_tokens, int32_t channels);
