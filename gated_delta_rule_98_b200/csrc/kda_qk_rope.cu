@@ -151,7 +151,7 @@ __device__ __forceinline__ Row turn(const Row& v, const float2 (&c)[2], const fl
 
 // across: lane groups along the heads (a power of two); the others take other tokens.
 template <typename T, int D, bool kPairs>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 5)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 4)
     qk_kernel(const QkArgs a, int tokens, int across) {
   constexpr int G = D / 8;            // lanes of a row
   constexpr int SLOTS = kThreads / G; // rows of a pass
@@ -177,6 +177,25 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 5)
 
   for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < a.T; t0 += (int64_t)gridDim.x * tokens) {
     const int count = (int)(a.T - t0 < tokens ? a.T - t0 : tokens);
+    // heads h0.. of token k0 + lane_token of the step: two rows of either side
+    Raw<T> next[2][U];
+    auto load = [&](int k0, int h0) {
+      const bool here = k0 + lane_token < count;
+      const int64_t t = t0 + (here ? k0 + lane_token : 0);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const QkSide& q = a.side[s];
+        const T* p = (const T*)q.x + t * q.x_stride + (h0 + lane_head) * D + o1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (here && h0 + u * across + lane_head < q.heads)
+            next[s][u].load(p + u * across * D, p + u * across * D + o2);
+          else
+            next[s][u].clear();
+        }
+      }
+    };
+    load(0, 0);
     __syncthreads();  // the last step's sines are read
     for (int i = threadIdx.x; i < count * half; i += kThreads) {
       // in turns, reduced to [-1/2, 1/2] in 64 bits; the rest fits 32
@@ -188,10 +207,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 5)
       s_sin[k][f] = sn;
     }
     __syncthreads();
-    for (int k0 = 0; k0 < count; k0 += side_by_side) {
-      const int k = k0 + lane_token;
+    for (int k0 = 0, h0 = 0; k0 < count;) {
+      Raw<T> x[2][U];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[s][u] = next[s][u];
+      const int at = h0, k = k0 + lane_token;
       const bool here = k < count;
-      const int64_t t = t0 + (here ? k : 0);
+      h0 += across * U;
+      if (h0 >= most) {
+        h0 = 0;
+        k0 += side_by_side;
+      }
+      if (k0 < count) load(k0, h0);
       float2 c[2], sn[2];
       if (turned) {
         const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[here ? k : 0][4 * l]);
@@ -201,46 +230,26 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 5)
         sn[0] = make_float2(s4.x, s4.y);
         sn[1] = make_float2(s4.z, s4.w);
       }
-      // this lane group's first head of either side; offsets of its rows from there
-      const T* px[2];
-      T* po[2];
+      const int64_t t = t0 + (here ? k : 0);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const QkSide& q = a.side[s];
-        px[s] = (const T*)q.x + t * q.x_stride + lane_head * D + o1;
-        po[s] = (T*)q.out + t * q.out_stride + lane_head * D + o1;
-      }
-      for (int h0 = 0; h0 < most; h0 += across * U) {
-        Raw<T> x[2][U];
+        T* p = (T*)q.out + t * q.out_stride + (at + lane_head) * D + o1;
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * across;
-            if (here && h + lane_head < a.side[s].heads) {
-              x[s][u].load(px[s] + h * D, px[s] + h * D + o2);
-            } else {
-              x[s][u].clear();
-            }
+        for (int u = 0; u < U; ++u) {
+          const int h = at + u * across;
+          if (h >= q.heads) break;
+          const Row v = x[s][u].template get<kPairs>();
+          const float rn = rsqrtf(row_sum<G>(dot(v, v)) * (1.f / D) + a.eps);
+          Row out = mul(v, scale(weight[s], rn));
+          if (turned) out = turn(out, c, sn);
+          if (here && h + lane_head < q.heads) {
+            float4 f1, f2;
+            groups_of<kPairs>(out, f1, f2);
+            st4(p + u * across * D, f1);
+            st4(p + u * across * D + o2, f2);
           }
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * across;
-            if (h >= a.side[s].heads) break;
-            const bool in = here && h + lane_head < a.side[s].heads;
-            const Row v = x[s][u].template get<kPairs>();
-            const float rn = rsqrtf(row_sum<G>(dot(v, v)) * (1.f / D) + a.eps);
-            Row out = mul(v, scale(weight[s], rn));
-            if (turned) out = turn(out, c, sn);
-            if (in) {
-              float4 f1, f2;
-              groups_of<kPairs>(out, f1, f2);
-              st4(po[s] + h * D, f1);
-              st4(po[s] + h * D + o2, f2);
-            }
-          }
+        }
       }
     }
   }
