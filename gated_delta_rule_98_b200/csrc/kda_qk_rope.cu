@@ -11,10 +11,11 @@
 // shuffles only for its sums, and a lane needs the sines of four angles
 // whatever the layout.  The sines of a token's rot/2 angles are formed once by
 // the block that owns the token and shared by all its heads.  A lane group goes
-// along the heads of one token, two of q and two of k at a time (one row at a
-// time, waiting for loads took 9 of 15 issue slots), so that weights and sines
-// are fixed while it does and a row costs few instructions besides its
-// arithmetic; the many resident blocks hide the rest.
+// along the heads of one token, two of q and two of k at a time with the next
+// ones on the way (16384 x (16 + 16) x 128 bf16: one row at a time 72 us, two 53,
+// with the next on the way 48, 86% of the copy rate).  With few heads the lane
+// groups take several tokens side by side.  Dealing rows out freely, each with
+// its own token and head, takes half as many instructions again (62 us).
 #include "kda_common.cuh"
 #include "kda_layer.h"
 
@@ -255,126 +256,133 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 4)
   }
 }
 
-// The gradient deals rows out freely, first the step's query heads, then its key
-// heads, each with its own token and head, the next two on the way while two are
-// worked on: more instructions a row than the forward's walk, but its two inputs
-// a row and its weight sums leave too few resident warps to hide the loads
-// otherwise (16384 x (16 + 16) x 128: 94 us; walking as the forward does, 106).
+// The gradient walks likewise, one side at a time (its two inputs a row take the
+// registers of the other side): 16384 x (16 + 16) x 128 bf16 88 us, 70% of the
+// copy rate; 94 with rows dealt out freely.
 template <typename T, int D, bool kPairs>
-__global__ void __launch_bounds__(kThreads)
-    qk_backward_kernel(const QkArgs a, int tokens, float* part) {
+__global__ void __launch_bounds__(kThreads, 4)
+    qk_backward_kernel(const QkArgs a, int tokens, int across, float* part) {
   constexpr int G = D / 8;            // lanes of a row
   constexpr int SLOTS = kThreads / G; // rows of a pass
-  constexpr int U = kRows, BATCH = SLOTS * U;
+  constexpr int U = kRows;
   __shared__ __align__(16) float s_cos[kMaxTokens][D / 2], s_sin[kMaxTokens][D / 2];
   __shared__ __align__(16) float s_dw[2][SLOTS][D];
+  __shared__ double s_freq[D / 2];  // turns per position
   const int l = threadIdx.x % G, slot = threadIdx.x / G;
   const int half = a.rot / 2;
   const bool turned = 8 * l < a.rot;
   const int o1 = !kPairs && turned ? 4 * l : 8 * l;
-  const int o2 = !kPairs && turned ? half + 4 * l : 8 * l + 4;
+  const int o2 = (!kPairs && turned ? half + 4 * l : 8 * l + 4) - o1;
+  const int lane_token = slot / across, lane_head = slot % across, side_by_side = SLOTS / across;
   Row weight[2], dw[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     Raw<float> w;
     w.a = w.b = make_float4(1.f, 1.f, 1.f, 1.f);
-    if (a.side[s].weight) w.load(a.side[s].weight + o1, a.side[s].weight + o2);
+    if (a.side[s].weight) w.load(a.side[s].weight + o1, a.side[s].weight + o1 + o2);
     weight[s] = w.template get<kPairs>();
     dw[s] = Row{{splat(0.f), splat(0.f)}, {splat(0.f), splat(0.f)}};
   }
-  const float per_head[2] = {1.f / max(a.side[0].heads, 1), 1.f / max(a.side[1].heads, 1)};
+  for (int i = threadIdx.x; i < half; i += kThreads) s_freq[i] = a.freqs[i] * 0.15915494309189533577;
+  const int first_side = a.side[0].heads > 0 ? 0 : 1;
+  const bool both = a.side[0].heads > 0 && a.side[1].heads > 0;
 
   for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < a.T; t0 += (int64_t)gridDim.x * tokens) {
     const int count = (int)(a.T - t0 < tokens ? a.T - t0 : tokens);
-    const int nq = (count * a.side[0].heads + BATCH - 1) / BATCH;
-    const int nb = nq + (count * a.side[1].heads + BATCH - 1) / BATCH;
-    Raw<T> x[U], d[U];
-    int tok[U], head[U];  // of the rows in x
-    // Batch b's rows; behind the last one zeros, and token -1.
-    auto load = [&](int b) {
-      const int s = b >= nq, heads = a.side[s].heads;
+    // heads h0.. of side s of token k0 + lane_token of the step
+    Raw<T> next_x[U], next_d[U];
+    auto load = [&](int k0, int s, int h0) {
+      const bool here = k0 + lane_token < count;
+      const int64_t t = t0 + (here ? k0 + lane_token : 0);
       const QkSide& q = a.side[s];
+      const int at = (h0 + lane_head) * D + o1;
+      const T* p = (const T*)q.x + t * q.x_stride + at;
+      const T* g = (const T*)q.dout + t * q.dout_stride + at;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int r = (b - (s ? nq : 0)) * BATCH + u * SLOTS + slot;
-        // r / heads, exactly: r < 16 heads + a batch stays below 2^20
-        const int k = (int)((r + 0.5f) * per_head[s]);
-        const int h = (r - k * heads) * D;
-        tok[u] = r < count * heads ? k : -1;
-        head[u] = h;
-        if (tok[u] >= 0) {
-          const T* p = (const T*)q.x + (t0 + k) * q.x_stride + h;
-          x[u].load(p + o1, p + o2);
-          const T* g = (const T*)q.dout + (t0 + k) * q.dout_stride + h;
-          d[u].load(g + o1, g + o2);
+        if (here && h0 + u * across + lane_head < q.heads) {
+          next_x[u].load(p + u * across * D, p + u * across * D + o2);
+          next_d[u].load(g + u * across * D, g + u * across * D + o2);
         } else {
-          x[u].clear();
-          d[u].clear();
+          next_x[u].clear();
+          next_d[u].clear();
         }
       }
     };
-    load(0);
+    load(0, first_side, 0);
     __syncthreads();  // the last step's sines are read
     for (int i = threadIdx.x; i < count * half; i += kThreads) {
       // in turns, reduced to [-1/2, 1/2] in 64 bits; the rest fits 32
-      const double turns = (double)a.positions[t0 + i / half] *
-                           (a.freqs[i % half] * 0.15915494309189533577);
+      const int k = i / half, f = i - k * half;
+      const double turns = (double)a.positions[t0 + k] * s_freq[f];
       float sn, cn;
       sincospif(2.f * (float)(turns - rint(turns)), &sn, &cn);
-      s_cos[i / half][i % half] = cn;
-      s_sin[i / half][i % half] = -sn;  // the gradient turns back
+      s_cos[k][f] = cn;
+      s_sin[k][f] = -sn;  // the gradient turns back
     }
     __syncthreads();
-    for (int b = 0; b < nb; ++b) {
-      const bool s = b >= nq;
-      const QkSide& q = a.side[s];
-      Row w, v[U], g[U];
-      int k[U], h[U];
+    for (int k0 = 0, s = first_side, h0 = 0; k0 < count;) {
+      Raw<T> x[U], d[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        x[u] = next_x[u];
+        d[u] = next_d[u];
+      }
+      const int at = h0, k = k0 + lane_token, side = s;
+      const bool here = k < count;
+      h0 += across * U;
+      if (h0 >= a.side[s].heads) {
+        h0 = 0;
+        if (both && s == 0) {
+          s = 1;
+        } else {
+          s = first_side;
+          k0 += side_by_side;
+        }
+      }
+      if (k0 < count) load(k0, s, h0);
+      const QkSide& q = a.side[side];
+      float2 c[2], sn[2];
+      if (turned) {
+        const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[here ? k : 0][4 * l]);
+        const float4 s4 = *reinterpret_cast<const float4*>(&s_sin[here ? k : 0][4 * l]);
+        c[0] = make_float2(c4.x, c4.y);
+        c[1] = make_float2(c4.z, c4.w);
+        sn[0] = make_float2(s4.x, s4.y);
+        sn[1] = make_float2(s4.z, s4.w);
+      }
+      Row w;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        w.lo[i] = s ? weight[1].lo[i] : weight[0].lo[i];
-        w.hi[i] = s ? weight[1].hi[i] : weight[0].hi[i];
+        w.lo[i] = side ? weight[1].lo[i] : weight[0].lo[i];
+        w.hi[i] = side ? weight[1].hi[i] : weight[0].hi[i];
       }
+      T* p = (T*)q.out + (t0 + (here ? k : 0)) * q.out_stride + (at + lane_head) * D + o1;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        v[u] = x[u].template get<kPairs>();
-        g[u] = d[u].template get<kPairs>();
-        k[u] = tok[u];
-        h[u] = head[u];
-      }
-      if (b + 1 < nb) load(b + 1);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool in = k[u] >= 0;
-        float2 c[2], sn[2];
-        if (turned) {
-          const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[in ? k[u] : 0][4 * l]);
-          const float4 s4 = *reinterpret_cast<const float4*>(&s_sin[in ? k[u] : 0][4 * l]);
-          c[0] = make_float2(c4.x, c4.y);
-          c[1] = make_float2(c4.z, c4.w);
-          sn[0] = make_float2(s4.x, s4.y);
-          sn[1] = make_float2(s4.z, s4.w);
-        }
-        const float rn = rsqrtf(row_sum<G>(dot(v[u], v[u])) * (1.f / D) + a.eps);
-        Row b_ = g[u];
-        if (turned) b_ = turn(b_, c, sn);
-        const Row vr = scale(v[u], rn);
+        const int h = at + u * across;
+        if (h >= q.heads) break;
+        const bool in = here && h + lane_head < q.heads;
+        const Row v = x[u].template get<kPairs>();
+        Row b = d[u].template get<kPairs>();
+        const float rn = rsqrtf(row_sum<G>(dot(v, v)) * (1.f / D) + a.eps);
+        if (turned) b = turn(b, c, sn);
+        const Row vr = scale(v, rn);
         if (in) {  // rn is inf off the rows at eps 0
-          if (s) dw[1] = fma(b_, vr, dw[1]);
-          else dw[0] = fma(b_, vr, dw[0]);
+          if (side) dw[1] = fma(b, vr, dw[1]);
+          else dw[0] = fma(b, vr, dw[0]);
         }
-        b_ = mul(b_, w);
+        b = mul(b, w);
         // r (c - v r^2 mean(c v)) = r c - (v r) r mean(c (v r))
-        const float m = row_sum<G>(dot(b_, vr)) * (-1.f / D) * rn;
+        const float m = row_sum<G>(dot(b, vr)) * (-1.f / D) * rn;
         Row ms;
         ms.lo[0] = ms.lo[1] = ms.hi[0] = ms.hi[1] = splat(m);
-        const Row out = fma(vr, ms, scale(b_, rn));
+        const Row out = fma(vr, ms, scale(b, rn));
         if (in) {
           float4 f1, f2;
           groups_of<kPairs>(out, f1, f2);
-          T* p = (T*)q.out + (t0 + k[u]) * q.out_stride + h[u];
-          st4(p + o1, f1);
-          st4(p + o2, f2);
+          st4(p + u * across * D, f1);
+          st4(p + u * across * D + o2, f2);
         }
       }
     }
@@ -385,7 +393,7 @@ __global__ void __launch_bounds__(kThreads)
       float4 f1, f2;
       groups_of<kPairs>(dw[s], f1, f2);
       st4(&s_dw[s][slot][o1], f1);
-      st4(&s_dw[s][slot][o2], f2);
+      st4(&s_dw[s][slot][o1 + o2], f2);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
@@ -432,21 +440,18 @@ cudaError_t launch_k(const QkArgs& a, bool back) {
   constexpr int SLOTS = kThreads / (D / 8);
   const int hq = a.side[0].heads, hk = a.side[1].heads;
   int tokens, blocks;
+  // lane groups along the heads: two heads of the larger side each, up to the
+  // block's; the others take tokens side by side
+  int across = 1;
+  while (across * kRows < (hq > hk ? hq : hk) && across < SLOTS) across *= 2;
+  steps_for(a.T, SLOTS / across, back ? kMaxBlocks : 148 * 64, tokens, blocks);
   if (!back) {
-    // lane groups along the heads: two heads of the larger side each, up to the
-    // block's; the others take tokens side by side
-    int across = 1;
-    while (across * kRows < (hq > hk ? hq : hk) && across < SLOTS) across *= 2;
-    steps_for(a.T, SLOTS / across, 148 * 64, tokens, blocks);
     qk_kernel<T, D, kPairs><<<blocks, kThreads, 0, a.stream>>>(a, tokens, across);
     return cudaGetLastError();
   }
-  // tokens until the smaller side's heads fill a batch
-  const int few = hq < 1 ? hk : hk < 1 || hq < hk ? hq : hk;
-  steps_for(a.T, (SLOTS * kRows + few - 1) / (few < 1 ? 1 : few), kMaxBlocks, tokens, blocks);
   const bool weights = a.side[0].dweight || a.side[1].dweight;
   qk_backward_kernel<T, D, kPairs>
-      <<<blocks, kThreads, 0, a.stream>>>(a, tokens, weights ? (float*)a.ws : nullptr);
+      <<<blocks, kThreads, 0, a.stream>>>(a, tokens, across, weights ? (float*)a.ws : nullptr);
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess || !weights) return err;
   qk_weight_kernel<<<2 * D, 128, 0, a.stream>>>((const float*)a.ws, blocks, D,
