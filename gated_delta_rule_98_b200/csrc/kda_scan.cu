@@ -103,6 +103,13 @@ __device__ __forceinline__ void decay(float2 t, float2& a, float2& m) {
   m.y = t.y > -0.2f ? q.y : 1.f - a.y;
 }
 
+// -e^A log2(e) of two channels, rounded once: sigmoid(u) far below 0 takes |u|
+// times the relative error of u = e^A z, so e^A gets none of its own.
+__device__ __forceinline__ float2 gate_scale(float2 A) {
+  return make_float2((float)(-1.4426950408889634 * exp((double)A.x)),
+                     (float)(-1.4426950408889634 * exp((double)A.y)));
+}
+
 // The library's gate on two channels: k = -e^A log2(e).
 struct GateZ {
   float2 a, m, p;  // decay, 1 - decay, s (1 - s)
@@ -393,7 +400,7 @@ __global__ void __launch_bounds__(kAlone * 32, 1)
 #pragma unroll
   for (int i = 0; i < D - 1; ++i) request(j0 + warp + i * W, i);
   float2 k = splat(0.f);
-  if (kZ && in && b.end > 0) k = make_float2(-kLog2e * expf(a.A[c]), -kLog2e * expf(a.A[c + 1]));
+  if (kZ && in && b.end > 0) k = gate_scale(*reinterpret_cast<const float2*>(a.A + c));
   Marker<true, SPAN> marker;
   int slot = 0;
   for (int j = j0 + warp; j < j1; j += W) {
@@ -565,7 +572,7 @@ __global__ void __launch_bounds__((kPair ? kPairedBack : kAloneBack) * 32, kPair
 #pragma unroll
   for (int i = 0; i < D - 1; ++i) request(j1 - 1 - warp - i * W, i);
   float2 k = splat(0.f);
-  if (kZ && in && b.end > 0) k = make_float2(-kLog2e * expf(a.A[c]), -kLog2e * expf(a.A[c + 1]));
+  if (kZ && in && b.end > 0) k = gate_scale(*reinterpret_cast<const float2*>(a.A + c));
   // -5 e^A, the constant factors of dz
   const float2 kz = __fmul2_rn(k, splat(-kGateMin / kLog2e));
   float2 dA = splat(0.f);
@@ -775,7 +782,7 @@ __global__ void __launch_bounds__(256)
   const int c = (int)(i % C);
   const float2 a = *reinterpret_cast<const float2*>(A + c);
   const float2 xv = lds2(x + i), zv = lds2(z + i), hv = lds2(h + i);
-  const GateZ g = gate_z<false>(zv, make_float2(-kLog2e * expf(a.x), -kLog2e * expf(a.y)));
+  const GateZ g = gate_z<false>(zv, gate_scale(a));
   const float2 v = __ffma2_rn(g.a, hv, __fmul2_rn(g.m, xv));
   stg2(h + i, v);
   stg2(y + i, v);

@@ -424,8 +424,9 @@ kda_status kda_short_conv_swish_backward(const void* x, const float* w, const vo
  *  workspace: kda_gated_scan_workspace_size bytes, 16-byte aligned, as in
  *             kda_forward.
  * The state, the products of a and every sum are float32 in a fixed order
- * (bit-identical from call to call).  One launch, two when few channels make
- * it split the token axis; the gradients one to three.
+ * (bit-identical from call to call); decays below 2^-126 count as 0.  One
+ * launch, two when few channels make it split the token axis; the gradients one
+ * to three.
  */
 #define KDA_SCAN_INTERVAL 32
 size_t kda_gated_scan_workspace_size(int32_t total_tokens, int32_t channels);

@@ -343,3 +343,10 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(y[-tail:], y1) and torch.equal(h[1:], h1)
     assert torch.equal(dx[-tail:], dx1) and torch.equal(dz[-tail:], dz1)
     assert torch.equal(dh0[1:], dh1) and (y[:100] == 0).all() and (y[-tail - 9:-tail] == 0).all()
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_gate_far_below_zero_keeps_its_accuracy(seed):
+    """sigmoid(u) near e^u takes |u| times the relative error of u = e^A z."""
+    p = make([120, 0, 77], 32, "f32", "z", seed=60 + 10 * seed, mean=-9.0, state=seed % 2 == 0)
+    check(p, *run(p))
