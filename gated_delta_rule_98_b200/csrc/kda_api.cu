@@ -611,6 +611,13 @@ kda_status kda_qk_norm_rope_backward(
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < kda_qk_norm_rope_backward_workspace_size(total_tokens, d))
     return KDA_ERR_INVALID_ARG;
+  if (total_tokens == 0 || (Hq == 0 && Hk == 0)) {
+    // no row: positions and freqs may be NULL, so no kernel may look at them
+    for (float* dw : {dq_weight, dk_weight})
+      if (dw && cudaMemsetAsync(dw, 0, (size_t)d * sizeof(float), a.stream) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    return KDA_OK;
+  }
   return kda::launch_qk_norm_rope_backward(a) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -516,7 +516,8 @@ kda_status kda_gated_scan_step(const void* x, const void* z, const float* A, flo
  *             (same stride); any other overlap is undefined.
  *  positions: [T] int32 (4-byte aligned).
  *  freqs    : [rot/2] float64, radians per position (8-byte aligned; may be
- *             NULL when rot is 0).
+ *             NULL when rot is 0).  Without tokens or heads neither positions
+ *             nor freqs is read, and both may be NULL.
  *  q_weight, k_weight : [d] float32 gains, 16-byte aligned, or NULL (ones).
  *  eps      : finite, not negative.
  *  T >= 0; Hq, Hk >= 0 (a side with no heads may be NULL), (Hq + Hk) * d at
@@ -544,6 +545,8 @@ kda_status kda_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int6
  *  dq_weight, dk_weight : [d] float32, overwritten, or NULL (not wanted).
  *  workspace: kda_qk_norm_rope_backward_workspace_size bytes, 16-byte aligned,
  *             as in kda_forward.
+ * Without tokens or heads nothing but the weight gradients is touched: they
+ * become 0, and positions and freqs may be NULL, as in the forward call.
  * Sums are float32 in a fixed order.  One launch, two with weight gradients.
  */
 size_t kda_qk_norm_rope_backward_workspace_size(int32_t total_tokens, int32_t d);

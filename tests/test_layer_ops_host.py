@@ -249,3 +249,32 @@ def test_binding_rejects_wrong_tensors():
               lambda: kda.qk_norm_rope_backward(q, k, q.bfloat16(), k, pos, freqs)):
         with pytest.raises(ValueError):
             f()
+
+
+def _qk_backward(T, Hq, Hk, pos, freqs, dqw=None, dkw=None, d=64, rot=32, ws=FAKE, stream=None):
+    """The rotation's gradient through the C ABI on fp32 rows that do not exist."""
+    nbytes = kda.kda_qk_norm_rope_backward_workspace_size(T, d)
+    return kda.kda_qk_norm_rope_backward(None, 0, None, 0, None, 0, None, 0, pos, freqs, None,
+                                         None, 1e-6, T, Hq, Hk, d, rot, 0, kda.KDA_F32, None, 0,
+                                         None, 0, dqw, dkw, ws, nbytes, stream)
+
+
+@pytest.mark.parametrize("T,Hq,Hk", [(0, 4, 2), (5, 0, 0), (0, 0, 0)])
+def test_rotation_gradient_without_rows_launches_nothing(T, Hq, Hk):
+    """positions and freqs are allowed to be NULL there: a kernel would read
+    address 0.  Without a GPU every launch fails, so KDA_OK means that there was none."""
+    assert _qk_backward(T, Hq, Hk, None, None) == kda.KDA_OK
+    assert _qk_backward(T, Hq, Hk, FAKE, FAKE) == kda.KDA_OK
+    assert _qk_backward(T, Hq, Hk, FAKE, None, ws=None) == BAD
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,Hq,Hk", [(0, 4, 2), (5, 0, 0), (0, 0, 0)])
+def test_rotation_gradient_without_rows_clears_the_weight_gradients(T, Hq, Hk):
+    ws = torch.empty(kda.kda_qk_norm_rope_backward_workspace_size(T, 64), dtype=torch.uint8,
+                     device="cuda")
+    dqw, dkw = torch.full((64,), 7.0, device="cuda"), torch.full((65,), 7.0, device="cuda")
+    st = _qk_backward(T, Hq, Hk, None, None, dqw.data_ptr(), dkw.data_ptr(), ws=ws.data_ptr(),
+                      stream=torch.cuda.current_stream().cuda_stream)
+    assert st == kda.KDA_OK
+    assert (dqw == 0).all() and (dkw[:64] == 0).all() and dkw[64] == 7
