@@ -684,6 +684,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 # workspaces they allocate belong to it (a freed workspace could otherwise be handed
 # out again while the kernels still use it).
 
+def _on(stream, t):
+    """``stream`` as the current one.  It has to be of t's GPU: the call runs on the
+    current stream of that GPU, which one of another GPU would not change."""
+    if stream.device != t.device:
+        raise ValueError(f"stream: on {stream.device}, the tensors are on {t.device}")
+    return torch.cuda.stream(stream)
+
+
 def _call(fn, device, *args):
     """Run a C entry point on GPU ``device`` and its current stream, and raise
     unless it returns KDA_OK."""
@@ -721,7 +729,7 @@ def short_conv_swish_backward(x, w, dy, *, cu_seqlens=None, num_seqs=None, max_s
     dtype).  Returns (dx, dw), dw [channels, width] fp32.  Rows from
     cu_seqlens[N] on (a padded batch) are left as they were in dx."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return short_conv_swish_backward(x, w, dy, cu_seqlens=cu_seqlens, num_seqs=num_seqs,
                                              max_seqlen=max_seqlen, dx=dx, dw=dw,
                                              workspace=workspace)
@@ -750,7 +758,7 @@ def short_conv_swish_backward(x, w, dy, *, cu_seqlens=None, num_seqs=None, max_s
 def _gated_scan(x, z, A, g, h0, cu_seqlens, num_seqs, max_seqlen, y, h_final, states,
                 save_states, ws, stream):
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return _gated_scan(x, z, A, g, h0, cu_seqlens, num_seqs, max_seqlen, y, h_final,
                                states, save_states, ws, None)
     T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
@@ -810,7 +818,7 @@ def gated_scan_g(x, g, *, h0=None, cu_seqlens=None, num_seqs=None, max_seqlen=No
 def _gated_scan_backward(x, z, A, g, states, dy, h0, dh_final, cu_seqlens, num_seqs, max_seqlen,
                          ws, stream):
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return _gated_scan_backward(x, z, A, g, states, dy, h0, dh_final, cu_seqlens,
                                         num_seqs, max_seqlen, ws, None)
     T, C, N, L = _packed(x, cu_seqlens, num_seqs, max_seqlen)
@@ -858,7 +866,7 @@ def gated_scan_step(x, z, A, h, *, y=None, stream=None):
     """One step of gated_scan for B sequences: x, z [B, ...], A [channels] fp32;
     h [B, channels] fp32 is updated in place.  Returns y (x's shape and dtype)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return gated_scan_step(x, z, A, h, y=y)
     B, C, _, _ = _packed(x, None, 1, None)
     dev, dt, f32, shape = x.get_device(), x.dtype, torch.float32, x.shape
@@ -913,7 +921,7 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     k may be slices of one projection's output (heads side by side, any token
     stride); q_out = q, k_out = k works in place.  Returns (q_out, k_out)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, q):
             return qk_norm_rope(q, k, positions, freqs, q_weight=q_weight, k_weight=k_weight,
                                 eps=eps, interleaved=interleaved, q_out=q_out, k_out=k_out)
     T, d, rot, read = _qk(q, k, positions, freqs, q_weight, k_weight)
@@ -942,7 +950,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, positions, freqs, *, q_weight=No
     (dq, dk, dq_weight, dk_weight), the last two [d] fp32 or None where the
     gain is None."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, q):
             return qk_norm_rope_backward(q, k, dq_out, dk_out, positions, freqs,
                                          q_weight=q_weight, k_weight=k_weight, eps=eps,
                                          interleaved=interleaved, dq=dq, dk=dk,

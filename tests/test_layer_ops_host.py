@@ -278,3 +278,22 @@ def test_rotation_gradient_without_rows_clears_the_weight_gradients(T, Hq, Hk):
                       stream=torch.cuda.current_stream().cuda_stream)
     assert st == kda.KDA_OK
     assert (dqw == 0).all() and (dkw[:64] == 0).all() and dkw[64] == 7
+
+
+def test_binding_rejects_a_stream_of_another_gpu():
+    """It would be made current on its own GPU, and the call would run on another stream."""
+    from types import SimpleNamespace
+    stream = SimpleNamespace(device=torch.device("cuda", 1))
+    x, A, st = torch.zeros(6, 16), torch.zeros(16), torch.zeros(1, 16)
+    q, pos = torch.zeros(6, 2, 32), torch.zeros(6, dtype=torch.int32)
+    freqs = torch.zeros(16, dtype=torch.float64)
+    for f in (lambda: kda.gated_scan(x, x, A, stream=stream),
+              lambda: kda.gated_scan_g(x, x, stream=stream),
+              lambda: kda.gated_scan_backward(x, x, A, st, x, stream=stream),
+              lambda: kda.gated_scan_g_backward(x, x, st, x, stream=stream),
+              lambda: kda.gated_scan_step(x, x, A, torch.zeros(6, 16), stream=stream),
+              lambda: kda.short_conv_swish_backward(x, torch.zeros(16, 4), x, stream=stream),
+              lambda: kda.qk_norm_rope(q, q, pos, freqs, stream=stream),
+              lambda: kda.qk_norm_rope_backward(q, q, q, q, pos, freqs, stream=stream)):
+        with pytest.raises(ValueError, match="stream"):
+            f()
