@@ -107,6 +107,10 @@ Offsets4 conv_offsets(size_t fw, size_t tok, int32_t dk, int32_t dv, size_t elt)
 
 bool opt_aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
+// Bounds of the packed [T, channels] operators with gradients: their kernels' token
+// and row-pitch arithmetic and the counts of their blocks are 32-bit (offsets are 64-bit).
+constexpr int32_t kMaxTokens = 0x7fffff00, kMaxChannels = 1 << 28;
+
 // Checks of the packed [T, channels] entry points (gated scan).
 kda_status check_scan(const void* x, const void* gate, const int32_t* cu, int32_t N, int32_t T,
                       int32_t max_len, int32_t channels, kda_dtype dt, const void* out,
@@ -114,8 +118,7 @@ kda_status check_scan(const void* x, const void* gate, const int32_t* cu, int32_
   if (dt != KDA_F32 && dt != KDA_BF16) return KDA_ERR_UNSUPPORTED;
   if (channels < 8 || channels % 8 != 0) return KDA_ERR_UNSUPPORTED;
   if (N < 0 || T < 0 || max_len < 0) return KDA_ERR_INVALID_ARG;
-  // the kernels' token and row-pitch arithmetic is 32-bit (offsets are 64-bit)
-  if (T > 0x7fffff00 || channels > (1 << 28)) return KDA_ERR_UNSUPPORTED;
+  if (T > kMaxTokens || channels > kMaxChannels) return KDA_ERR_UNSUPPORTED;
   if (!cu && (int64_t)N * max_len != T) return KDA_ERR_INVALID_ARG;
   if (N == 0 && T > 0) return KDA_ERR_INVALID_ARG;
   if (!opt_aligned4(cu)) return KDA_ERR_INVALID_ARG;
@@ -452,6 +455,7 @@ kda_status kda_short_conv_swish(const void* x, const float* w, const int32_t* cu
 size_t kda_short_conv_swish_backward_workspace_size(int32_t total_tokens, int32_t channels,
                                                     int32_t width) {
   if (total_tokens < 0 || channels < 8 || channels % 8 != 0 || width < 1 || width > 4) return 0;
+  if (total_tokens > kMaxTokens || channels > kMaxChannels) return 0;
   return kda::conv_backward_workspace_bytes(total_tokens, channels, width);
 }
 
@@ -466,8 +470,7 @@ kda_status kda_short_conv_swish_backward(const void* x, const float* w, const vo
   if (width < 1 || width > 4) return KDA_ERR_UNSUPPORTED;
   if (channels < 8 || channels % 8 != 0) return KDA_ERR_UNSUPPORTED;
   if (num_seqs < 0 || total_tokens < 0 || max_seqlen < 0) return KDA_ERR_INVALID_ARG;
-  // the kernel's token arithmetic is 32-bit (offsets are 64-bit)
-  if (total_tokens > 0x7fffff00) return KDA_ERR_UNSUPPORTED;
+  if (total_tokens > kMaxTokens || channels > kMaxChannels) return KDA_ERR_UNSUPPORTED;
   if (!cu_seqlens && (int64_t)num_seqs * max_seqlen != total_tokens) return KDA_ERR_INVALID_ARG;
   if (total_tokens > 0 && num_seqs == 0) return KDA_ERR_INVALID_ARG;
   if (!w || !dw || !opt_aligned4(w) || !opt_aligned4(dw) || !opt_aligned4(cu_seqlens))
@@ -485,6 +488,7 @@ kda_status kda_short_conv_swish_backward(const void* x, const float* w, const vo
 
 size_t kda_gated_scan_workspace_size(int32_t total_tokens, int32_t channels) {
   if (total_tokens < 0 || channels < 8 || channels % 8 != 0) return 0;
+  if (total_tokens > kMaxTokens || channels > kMaxChannels) return 0;
   return kda::scan_workspace_bytes(total_tokens, channels);
 }
 

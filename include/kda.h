@@ -381,8 +381,8 @@ kda_status kda_short_conv_swish(const void* x, const float* w, const int32_t* cu
  *  workspace : kda_short_conv_swish_backward_workspace_size bytes, 16-byte
  *              aligned, as in kda_forward.
  * u is recomputed from x.  Sums are float32 in a fixed order (bit-identical
- * from call to call).  total_tokens at most 2^31 - 256 (else
- * KDA_ERR_UNSUPPORTED).  One or two launches.
+ * from call to call).  total_tokens at most 2^31 - 256, channels at most 2^28
+ * (else KDA_ERR_UNSUPPORTED, and the size is 0).  One or two launches.
  */
 size_t kda_short_conv_swish_backward_workspace_size(int32_t total_tokens, int32_t channels,
                                                     int32_t width);
@@ -420,7 +420,7 @@ kda_status kda_short_conv_swish_backward(const void* x, const float* w, const vo
  *             cu_seqlens[N] may lie below total_tokens (a padded batch): rows
  *             from there on are not read, and y keeps what it held there.
  *  channels : a positive multiple of 8, at most 2^28; total_tokens at most
- *             2^31 - 256 (else KDA_ERR_UNSUPPORTED).
+ *             2^31 - 256 (else KDA_ERR_UNSUPPORTED, and the size is 0).
  *  workspace: kda_gated_scan_workspace_size bytes, 16-byte aligned, as in
  *             kda_forward.
  * The state, the products of a and every sum are float32 in a fixed order

@@ -297,3 +297,19 @@ def test_binding_rejects_a_stream_of_another_gpu():
               lambda: kda.qk_norm_rope_backward(q, q, q, q, pos, freqs, stream=stream)):
         with pytest.raises(ValueError, match="stream"):
             f()
+
+
+@pytest.mark.parametrize("C", [(1 << 28) + 8, (1 << 31) - 8])
+def test_channels_beyond_the_launch_arithmetic_are_refused(C):
+    """Counting the blocks of 2^31 - 8 channels passes 32 bits; the sizes say 0 for
+    what the calls refuse, and for the largest sizes that they take they do not."""
+    big = 1 << 60
+    assert kda.kda_short_conv_swish_backward(FAKE, FAKE, FAKE, None, 1, 1, 1, C, 4, kda.KDA_F32,
+                                             FAKE, FAKE, FAKE, big, None) == UNS
+    assert _scan("z", C=C, wsb=big) == UNS and _scan("g", True, C=C, wsb=big) == UNS
+    for T, size in ((1, C), (0x7fffff01, 8)):
+        assert kda.kda_short_conv_swish_backward_workspace_size(T, size, 4) == 0
+        assert kda.kda_gated_scan_workspace_size(T, size) == 0
+    for T, size in ((1, 1 << 28), (0x7fffff00, 8), (0x7fffff00, 1 << 28)):
+        assert kda.kda_short_conv_swish_backward_workspace_size(T, size, 4) >= 16 * size
+        assert kda.kda_gated_scan_workspace_size(T, size) >= 12 * size
