@@ -350,3 +350,58 @@ def test_gate_far_below_zero_keeps_its_accuracy(seed):
     """sigmoid(u) near e^u takes |u| times the relative error of u = e^A z."""
     p = make([120, 0, 77], 32, "f32", "z", seed=60 + 10 * seed, mean=-9.0, state=seed % 2 == 0)
     check(p, *run(p))
+
+
+def check_channels(p, out, grads, idx):
+    """check() on the channels ``idx`` alone (the recurrence does not mix channels)."""
+    T, cut = p["T"], torch.as_tensor(idx)
+    q = {k: v[..., cut] if torch.is_tensor(v) and k != "cu" else v for k, v in p.items()}
+    on = lambda t: t.index_select(t.dim() - 1, cut.to(t.device))
+    assert q["x"].shape == (T, len(idx))
+    check(q, tuple(on(t) for t in out), tuple(on(t) for t in grads))
+
+
+def some_channels(C, seed, n=48):
+    """The first and last columns of channels, and some between."""
+    rng = np.random.default_rng(seed)
+    return sorted({*range(8), *range(C - 8, C), *rng.choice(C, min(n, C), replace=False).tolist()})
+
+
+# Sequences of a long axis: one alone, or starts at every offset from a span's
+# first token, some next to each other, with a long one last.
+def long_axis(T, packed, seed):
+    if not packed:
+        return [T]
+    rng = np.random.default_rng(seed)
+    lens = [1, 0, 31, 32, 33, 63, 64, 65, 1, 1]
+    while sum(lens) < T // 2:
+        lens.append(int(rng.integers(1, T // 12)))
+    return lens + [T - sum(lens)]
+
+
+# Sizes by what a launch does with them: a block alone on its SM (channel groups times
+# segments at most 148) or one of two, the token axis whole or cut, and many more spans
+# a warp than it has slots, so that every slot is filled again several times.
+LONG = [
+    ("bf16", 3000, 1192),    # alone, whole: 94 spans over 12 or 15 warps
+    ("f32", 6000, 600),
+    ("bf16", 3000, 2400),    # paired, whole: 94 spans over 8 warps
+    ("f32", 4000, 1208),
+    ("bf16", 20000, 512),    # paired, 9 segments of 70 spans
+    ("f32", 20000, 264),     # paired, 8 segments of 40 spans
+    ("bf16", 6000, 512),     # paired, 9 segments of 21 spans
+    ("f32", 4099, 264),      # paired, 8 segments of 9 spans
+    ("bf16", 80000, 32),     # alone, 63 segments of 40 spans
+    ("f32", 80000, 16),      # alone, 63 segments of 20 spans
+]
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("entry", ["z", "g"])
+@pytest.mark.parametrize("dtype,T,C", LONG)
+def test_long_axes_in_every_launch_form(dtype, T, C, entry, packed):
+    seed = T + C + packed
+    lens = long_axis(T, packed, seed)
+    assert sum(lens) == T and min(lens) >= 0
+    p = make(lens, C, dtype, entry, seed=seed, state=packed)
+    check_channels(p, *run(p), some_channels(C, seed))
