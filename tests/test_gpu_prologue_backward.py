@@ -1,5 +1,6 @@
 """Gradient of the input prologue on the GPU against the float64 oracle, within
 the bound that the oracle carries for a float32 evaluation."""
+import numpy as np
 import pytest
 import torch
 
@@ -139,3 +140,79 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(dx[-tail:], dx1) and (dx[:100] == 0).all()
     # dw's sums are grouped otherwise: tail terms of magnitude |du x|, each rounded
     assert ((dw - dw1).abs() <= tail * 2.0 ** -24 * 30).all()
+
+
+# What one run of a warp holds (the longest of 8 to 128 tokens that still gives enough
+# blocks: 240 of bf16, 120 of fp32; a block has 8 runs of 128 channels): more groups of
+# 8 tokens than the warp has slots, so that every slot is filled again.
+RUNS = [
+    ("bf16", 1100, 3840, 16), ("bf16", 1100, 7680, 32), ("bf16", 1100, 12808, 64),
+    ("bf16", 1100, 15368, 128), ("f32", 1100, 1920, 16), ("f32", 1100, 3840, 32),
+    ("f32", 1100, 6408, 64), ("f32", 1100, 7688, 128),
+]
+
+
+def check_channels(p, dx, dw, seed, n=40):
+    """check() on some channels alone (the prologue does not mix channels)."""
+    C, rng = p["x"].shape[1], np.random.default_rng(seed)
+    idx = torch.tensor(sorted({*range(4), *range(C - 8, C),
+                               *rng.choice(C, min(n, C), replace=False).tolist()}))
+    q = dict(p, x=p["x"][:, idx], dy=p["dy"][:, idx], w=p["w"][idx])
+    check(q, dx[:, idx.cuda()], dw[idx.cuda()])
+
+
+@pytest.mark.parametrize("W", [1, 2, 3, 4])
+@pytest.mark.parametrize("dtype,T,C,run", RUNS)
+def test_every_length_of_a_run(dtype, T, C, run, W):
+    """Runs that cross no sequence start, and starts in a run's first, middle and last
+    groups, at every offset in a group."""
+    lens = [3 * run + 5, 1, 2, 8, 7, 9, 40, 3, 0, 1, 1, 25]
+    if sum(lens) < T:
+        lens.append(T - sum(lens))
+    p = make(lens, C, W, dtype, seed=run + W, pad=T - sum(lens))
+    dx, dw = kda.short_conv_swish_backward(cuda(p["x"]), cuda(p["w"]), cuda(p["dy"]),
+                                           cu_seqlens=cuda(p["cu"]), max_seqlen=p["L"])
+    check_channels(p, dx, dw, seed=run)
+    q = make([T], C, W, dtype, seed=run + W + 50)
+    dx, dw = kda.short_conv_swish_backward(cuda(q["x"]), cuda(q["w"]), cuda(q["dy"]))
+    check_channels(q, dx, dw, seed=run)
+
+
+@pytest.mark.parametrize("dtype,W", [("bf16", 4), ("f32", 3)])
+def test_blocks_that_take_a_second_tile(dtype, W):
+    """More tokens than 512 blocks of 8 runs of 128: a block goes on with the next tile.
+    Against the definition in 64 bits, shifted tensors instead of loops; the bound is
+    the oracle's, 32 units of 2^-24 of every term."""
+    T, C, U = 512 * 8 * 128 + 12345, 8, scan.U
+    x, dy, w = draw(70, dtype, T, C), draw(71, dtype, T, C), draw(72, "f32", C, W, std=W ** -0.5)
+    starts = [0, 128, 129, 1024, 300001, T - 12345, T - 12340, T - 1]
+    cu = torch.tensor([*starts, T], dtype=torch.int32)
+    dx, dw = kda.short_conv_swish_backward(x.cuda(), w.cuda(), dy.cuda(), cu_seqlens=cu.cuda(),
+                                           max_seqlen=T)
+    x, dy, w = x.double(), dy.double(), w.double()
+    seq = torch.zeros(T, dtype=torch.int64)
+    seq[torch.tensor(starts)] = 1
+    seq = seq.cumsum(0)
+
+    def earlier(v, j):                  # row t: v of token t - j of the same sequence, or 0
+        out = torch.zeros_like(v)
+        out[j:] = v[:T - j] * (seq[j:] == seq[:T - j])[:, None] if j else v
+        return out
+
+    def later(v, j):
+        out = torch.zeros_like(v)
+        out[:T - j] = v[j:] * (seq[j:] == seq[:T - j])[:, None] if j else v
+        return out
+
+    terms = [w[:, W - 1 - j] * earlier(x, j) for j in range(W)]
+    u, e_u = sum(terms), 32 * U * sum(t.abs() for t in terms)
+    p = torch.sigmoid(u)
+    du = dy * p * (1 + u * (1 - p))
+    e_du = dy.abs() * (0.5 * e_u + 32 * U * p * (1 + u.abs() * (1 - p)))
+    want = sum(w[:, W - 1 - j] * later(du, j) for j in range(W))
+    bound = sum(w[:, W - 1 - j].abs() * later(e_du + 32 * U * du.abs(), j) for j in range(W))
+    close(dx, want.numpy(), bound.numpy(), "dx")
+    want = torch.stack([(du * earlier(x, j)).sum(0) for j in reversed(range(W))], 1)
+    bound = torch.stack([((e_du + 64 * U * du.abs()) * earlier(x, j).abs()).sum(0)
+                         for j in reversed(range(W))], 1)
+    close(dw, want.numpy(), bound.numpy(), "dw")
