@@ -403,7 +403,7 @@ kda_status kda_short_conv_swish_backward(const void* x, const float* w, const vo
  *
  * so h stays between the extremes of h0 and x but for rounding: whatever the
  * gates, a constant drifts by no more than 0.03% over 65536 tokens with bf16
- * and 0.002% with float32 (measured at gates from 1e-9 to 0.5).  1 - a_t is
+ * and 0.003% with float32 (measured at gates from 1e-9 to 0.5).  1 - a_t is
  * taken as -expm1(g_t), and products of a_t near 1 by their complements.
  *
  *  x, z, y  : [T, channels] in `dt`; y must not overlap any input.
@@ -426,7 +426,10 @@ kda_status kda_short_conv_swish_backward(const void* x, const float* w, const vo
  *  workspace: kda_gated_scan_workspace_size bytes, 16-byte aligned, as in
  *             kda_forward.
  * The state, the products of a and every sum are float32 in a fixed order
- * (bit-identical from call to call); decays below 2^-126 count as 0.  One
+ * (bit-identical from call to call); decays below 2^-126 count as 0.  The
+ * arguments of the exponentials are rounded to float32: with u = exp(A) z far
+ * below 0, 1 - a_t is off by up to 2 |u| + 32 units of 2^-24 of itself (and
+ * exp(g_t) by 1.3 |g_t| + 32), no more than u's own steps in float32.  One
  * launch, two when few channels make it split the token axis; the gradients one
  * to three.
  */

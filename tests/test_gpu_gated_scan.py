@@ -507,3 +507,47 @@ def test_growing_states_keep_the_product():
     p["g"][:, ::3] = 1e-3
     p["g"][:, 1::3] = 0.0
     check(p, *run(p))
+
+
+def _tail_check(got, want, units, what):
+    """Relative to the value; results next to 2^-126 may be flushed."""
+    g, ok = got.cpu().double().numpy(), np.abs(want) > 1e-36
+    assert (np.abs(g[~ok]) <= 2e-36).all() and ok.sum() > 1000, what
+    close(torch.from_numpy(g[ok]).to(got.dtype), want[ok], (units * scan.U * np.abs(want))[ok], what)
+
+
+@pytest.mark.parametrize("mean", [-4, -9, -20, -40, -60])
+def test_tail_of_the_gate(mean):
+    """1 - a and the slope from thousands of first tokens with u down to -100: u = e^A z
+    has two roundings, each of at most one unit of 2^-24 of itself, and the exponential
+    takes |u| times that; 32 units for the rest (the slope: 64, it has both factors)."""
+    N, C = 256, 1024
+    z = draw(100 - mean, "f32", N, C, mean=mean, std=1.5)
+    A = draw(200 - mean, "f32", C, std=0.3)
+    u = np.exp(scan.f64(A)) * scan.f64(z)
+    s, units = scan.sigmoid(u), 32 + 2 * np.abs(u)
+    m = -np.expm1(-5 * s)
+    one, zg, Ag = torch.ones(N, C, device="cuda"), z.cuda(), A.cuda()
+    y = kda.gated_scan_step(one, zg, Ag, torch.zeros(N, C, device="cuda"))
+    _tail_check(y, m, units, "step")
+    how = dict(num_seqs=N)
+    y, h, states = kda.gated_scan(one, zg, Ag, save_states=True, **how)
+    _tail_check(y, m, units, "y")
+    _tail_check(h, m, units, "h_final")
+    dx, dz, _, _ = kda.gated_scan_backward(one, zg, Ag, states, one, **how)
+    _tail_check(dx, m, units, "dx")
+    # h_{t-1} - x = -1 and l = 1: dz = 5 s (1 - s) e^A a
+    want = 5 * s * scan.sigmoid(-u) * np.exp(scan.f64(A)) * np.exp(-5 * s)
+    _tail_check(dz, want, units + 32, "dz")
+
+
+def test_tail_of_a_given_decay():
+    """exp(g) takes g log2(e) in float32: a rounding of at most one unit of itself, and a
+    quarter of one for the constant's; 32 units for the rest."""
+    N, C = 256, 1024
+    g = -torch.exp(draw(7, "f32", N, C, mean=2.0, std=1.0))
+    one, zero = torch.ones(N, C, device="cuda"), torch.zeros(N, C, device="cuda")
+    y, h = kda.gated_scan_g(zero, g.cuda(), h0=one, num_seqs=N)
+    want = np.exp(scan.f64(g))
+    _tail_check(y, want, 32 + 1.25 * np.abs(scan.f64(g)), "y")
+    _tail_check(h, want, 32 + 1.25 * np.abs(scan.f64(g)), "h_final")
