@@ -429,7 +429,9 @@ kda_status kda_short_conv_swish_backward(const void* x, const float* w, const vo
  * (bit-identical from call to call); decays below 2^-126 count as 0.  The
  * arguments of the exponentials are rounded to float32: with u = exp(A) z far
  * below 0, 1 - a_t is off by up to 2 |u| + 32 units of 2^-24 of itself (and
- * exp(g_t) by 1.3 |g_t| + 32), no more than u's own steps in float32.  One
+ * exp(g_t) by 1.3 |g_t| + 32), no more than u's own steps in float32.  A
+ * state that is infinite or NaN stays one of the two to its sequence's end
+ * (0 * inf where a product of decays has become 0) and reaches no other.  One
  * launch, two when few channels make it split the token axis; the gradients one
  * to three.
  */
@@ -461,7 +463,8 @@ kda_status kda_gated_scan_g(const void* x, const float* g, const float* h0,
  *   l_t  = dy_t + a_{t+1} l_{t+1}          (the last token: dy_t + dh_final)
  *   dx_t = (1 - a_t) l_t
  *   dz_t = -5 s_t (1 - s_t) exp(A) a_t (h_{t-1} - x_t) l_t
- *   dA   = sum over all tokens of dz_t z_t (before dz is rounded)
+ *   dA   = sum over all tokens of dz_t z_t (before dz is rounded; an infinite
+ *          z makes its channel's sum NaN, 0 * inf)
  *   dh0  = a_first l_first                 (an empty sequence: dh_final)
  *
  *  x, z, A, h0, states, cu_seqlens, sizes : as given to (states: as written

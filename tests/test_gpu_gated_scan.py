@@ -551,3 +551,24 @@ def test_tail_of_a_given_decay():
     want = np.exp(scan.f64(g))
     _tail_check(y, want, 32 + 1.25 * np.abs(scan.f64(g)), "y")
     _tail_check(h, want, 32 + 1.25 * np.abs(scan.f64(g)), "h_final")
+
+
+@pytest.mark.parametrize("entry", ["z", "g"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinite_states_with_strong_gates_stay_in_their_sequence(dtype, entry):
+    """Products of strong decays become 0: an infinite state is then infinite or NaN to
+    the end of its sequence, and no other sequence or channel changes."""
+    p = make([50, 700, 90], 16, dtype, entry, seed=97)
+    if entry == "z":
+        p["z"][:] = p["z"].abs() + 2
+    else:
+        p["g"][:] = p["g"] - 5
+    clean, _ = run(p)
+    p["x"][60, 5] = float("inf")
+    p["x"][70, 9] = float("nan")
+    out, _ = run(p)
+    y, keep = out[0].cpu().float(), torch.ones(840, 16, dtype=torch.bool)
+    keep[60:750, 5] = keep[70:750, 9] = False
+    assert not torch.isfinite(y[~keep]).any()
+    assert torch.equal(out[0].cpu()[keep], clean[0].cpu()[keep])
+    assert not torch.isfinite(out[1][1, [5, 9]]).any() and torch.isfinite(out[1][2]).all()
