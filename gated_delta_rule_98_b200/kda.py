@@ -15,6 +15,11 @@ the current stream: ``forward``, ``forward_g``, ``forward_scalar_gate``,
 ``_backward``, ``gated_scan_step``, ``qk_norm_rope`` and its ``_backward``,
 ``cp_local`` / ``cp_finish`` / ``state_compose`` (context parallelism; the
 collective lives in ``cp.py``), ``workspace`` and ``check_device_error``.
+
+No helper builds an autograd graph: outputs do not require gradients, whatever
+the inputs do.  Where a ``_backward`` helper exists, the caller calls it with the
+gradient of the output (from a ``torch.autograd.Function`` of their own, if they
+want torch to do so).
 """
 from __future__ import annotations
 
@@ -618,7 +623,8 @@ def decode_step_norm_gate(q, k, v, z, A, beta, S, out_gate, *, norm_weight=None,
 def short_conv_swish(x, w, *, cu_seqlens=None, num_seqs=None, max_seqlen=None, y=None,
                      stream=None):
     """Input prologue on one tensor x [T, ...] (trailing axes = channels):
-    y = Swish(causal depthwise convolution with taps w [channels, width])."""
+    y = Swish(causal depthwise convolution with taps w [channels, width]).  No
+    autograd graph is built: short_conv_swish_backward gives the gradients."""
     _check_cuda(x, w, cu_seqlens, y)
     T = x.shape[0]
     C = x.numel() // T if T else int(np.prod(x.shape[1:]))
@@ -801,7 +807,8 @@ def gated_scan(x, z, A, *, h0=None, cu_seqlens=None, num_seqs=None, max_seqlen=N
     [N, channels] fp32 or None.  Returns (y, h_final), and with ``save_states``
     also the states that gated_scan_backward needs,
     [ceil(T / KDA_SCAN_INTERVAL), channels] fp32.  Rows from cu_seqlens[N] on
-    (a padded batch) are left as they were in y."""
+    (a padded batch) are left as they were in y.  No autograd graph is built:
+    gated_scan_backward gives the gradients."""
     return _gated_scan(x, z, A, None, h0, cu_seqlens, num_seqs, max_seqlen, y, h_final, states,
                        save_states, workspace, stream)
 
@@ -810,7 +817,7 @@ def gated_scan_g(x, g, *, h0=None, cu_seqlens=None, num_seqs=None, max_seqlen=No
                  save_states=False, y=None, h_final=None, states=None, workspace=None,
                  stream=None):
     """gated_scan with the fp32 log-decay g (x's shape) given directly and the
-    input unscaled: h_t = exp(g_t) h_{t-1} + x_t."""
+    input unscaled: h_t = exp(g_t) h_{t-1} + x_t.  Gradients: gated_scan_g_backward."""
     return _gated_scan(x, None, None, g, h0, cu_seqlens, num_seqs, max_seqlen, y, h_final,
                        states, save_states, workspace, stream)
 
@@ -919,7 +926,9 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     rotation by positions [T] int32 times freqs [rot/2] fp64 of the first rot
     channels, paired (i, i + rot/2), or (2i, 2i+1) when ``interleaved``.  q and
     k may be slices of one projection's output (heads side by side, any token
-    stride); q_out = q, k_out = k works in place.  Returns (q_out, k_out)."""
+    stride); q_out = q, k_out = k works in place.  Returns (q_out, k_out).  No
+    autograd graph is built: qk_norm_rope_backward gives the gradients, from q and
+    k as they were before."""
     if stream is not None:
         with _on(stream, q):
             return qk_norm_rope(q, k, positions, freqs, q_weight=q_weight, k_weight=k_weight,
