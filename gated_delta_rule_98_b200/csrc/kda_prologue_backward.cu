@@ -15,9 +15,9 @@
 // take 8 runs that follow one another and add their dw through shared memory;
 // the blocks' sums are added by a second launch, in a fixed order.
 //
-// Measured, W = 4: 32768 x 6144 bf16 235 us (5.1 TB/s, 78% of the copy rate: 56% of
-// the issue slots, 39% of the special function unit), 16384 x 4096 fp32 133 us (6.1
-// TB/s, 93%).
+// Measured, W = 4: 32768 x 6144 bf16 233 us (5.2 TB/s, 79% of the copy rate: 56% of
+// the issue slots, 39% of the special function unit), 16384 x 4096 fp32 134 us (6.0
+// TB/s, 92%).
 #include "kda_common.cuh"
 #include "kda_layer.h"
 

@@ -34,9 +34,9 @@
 // that the forward saved at every span, in 32 bits, instead of being read back
 // as rounded y (2 bytes an element less to read, and no second rounding).
 //
-// Measured: 65536 x 2048 bf16 forward 195 us (4.1 TB/s), gradient 340 us (3.9);
-// 32768 x 4096 forward 195 us, gradient 336 us (4.0); 16384 x 2048 fp32 87 us (4.6)
-// and 155 us (4.3).  Bound by the latency and issue of the gates' arithmetic (65%
+// Measured: 65536 x 2048 bf16 forward 200 us (4.0 TB/s), gradient 343 us (3.9);
+// 32768 x 4096 forward 201 us, gradient 340 us (3.9); 16384 x 2048 fp32 88 us (4.6)
+// and 156 us (4.3).  Bound by the latency and issue of the gates' arithmetic (65%
 // of the issue slots), not by the hand-over: without it the times are the same.
 #include <type_traits>
 
@@ -196,8 +196,8 @@ __device__ __forceinline__ Map compose(Map& run, int lane) {
 //    194 -> 200 us, gradient 340 -> 343);
 //  * fp32 takes the state over the whole span as h + (H - q h), q from the sum of the
 //    logarithms, rounded once to h's digits: a drift of 0.002%.  It costs 1% there
-//    (16384 x 2048: 87 -> 88 us, 155 -> 156), but lengthens the chain of warps, which
-//    bounds the forward in bf16 (250 us), whose outputs hold 8 bits.
+//    (16384 x 2048: 87 -> 88 us, 155 -> 156), where the loads leave time; in bf16 it
+//    took 250 us at 65536 x 2048, and the outputs hold 8 bits.
 // A segment's map has its product from the sum of the logarithms too.
 
 // Sum over a span of its runs' sums of log2 a (LC lanes each).
@@ -896,11 +896,12 @@ __global__ void __launch_bounds__(256)
 // ----------------------------------------------------------------- launch ----
 
 // Segments of the token axis.  None where the channels alone give a block to half
-// the SMs: the maps' launch costs more than the idle SMs (32768 x 1408 bf16: 103 us
-// in one segment, 127 in three; 32768 x 1024: 103 and 100, its gradient 168 and
-// 143).  Below, two blocks per SM (32768 x 512: 53 us with 296 blocks, 67 with 148,
-// 63 with 444), segments of 512 tokens at least (4096 x 256: 14.7 us, with 1024
-// 17.9; 256 gains 2 us more there and costs short calls a launch).
+// the SMs: the maps' launch costs more than the idle SMs, forward and gradient (bf16,
+// 32768 x 1408 in one segment 105 and 172 us, in three 130 and 176; x 2048 in one 105
+// and 179, in two 170 and 251; x 1024 in one 102 and 167, in four 98 and 132).  Below,
+// two blocks per SM (32768 x 512: 51 and 68 us with 288 blocks, 64 and 84 with 128, 62
+// and 89 with 416), segments of 512 tokens at least (4096 x 256: 15.3 and 21.1 us, with
+// 1024 17.8 and 24.0; 256 gains 0.5 and 0.9 and costs shorter calls a launch).
 int segments(int T, int cols) {
   if (cols >= 74) return 1;
   const int s = 296 / cols < T / 512 ? 296 / cols : T / 512;
